@@ -23,6 +23,11 @@
  *    (the engine refuses to start over budget); here: every call validates its
  *    arguments on the host and returns a status before launching anything.
  *
+ *  - A ring buffer / sliding window "to keep latency stable".  Page "標籤: vLLM",
+ *    section 2.  The calls above attend to the whole context; a caller that
+ *    bounds it uses nf_decode_attn_window / nf_prefill_attn_window, and the
+ *    page calls (nf_kv_reserve ... nf_kv_compact) to turn the segments.
+ *
  * Conventions for every call:
  *  - The caller owns every buffer (pool planes, block tables, lengths, q, out,
  *    workspace).  The library never allocates, frees or synchronises; all work
@@ -69,6 +74,11 @@ typedef int32_t nf_status;
                                  alignment); the call did no work */
 #define NF_DEVERR_RANGE 6     /* nf_prefill_attn: a K or V scale whose dequantised codes leave the
                                  fp16 range the kernel computes in (the results are not finite) */
+#define NF_DEVERR_CONFLICT 7  /* nf_kv_fork, nf_kv_copy_blocks: a pair whose destination is another
+                                 pair's source or destination (the pair was not carried out) */
+#define NF_DEVERR_POOL 8      /* nf_kv_reserve, nf_kv_fork: not enough free blocks */
+#define NF_DEVERR_REFS 9      /* nf_kv_release, nf_kv_fork, nf_kv_compact: a table entry that no count
+                                 in refs stands for */
 
 /* Element types. */
 #define NF_F32 0
@@ -354,6 +364,193 @@ nf_status nf_prefill_attn(const nf_kv_layer *kv, const void *q, int32_t q_dtype,
                           int32_t max_blocks, const int32_t *seqlens, int32_t max_seqlen,
                           float softmax_scale, int32_t causal, float *out, float *out_lse,
                           nf_stream_t stream);
+
+/*
+ * nf_decode_attn_window -- nf_decode_attn with a sliding window and sinks.
+ *
+ * Query j of sequence b sits at position P = seqlens[b] - n_q + j and sees the
+ * keys t <= P with t > P - window (the window, its own position included) or
+ * t < n_sink (the first tokens, which stay visible); a key that is both counts
+ * once.  window >= 1, n_sink >= 0; a window of at least seqlens[b] is full
+ * causal attention.  Arguments, layouts, formats and numerics as for
+ * nf_decode_attn, with these differences:
+ *   out is of out_dtype: NF_F32, or NF_BF16 (each value rounded once);
+ *     16-byte aligned.  out_lse is fp32 or NULL.
+ *   seqlens[b] == 0 marks an unused row of the batch: its rows come out o = 0,
+ *     lse = -inf and no error is recorded; other lengths below n_q or above
+ *     max_seqlen are NF_DEVERR_SEQLEN as before.
+ *   Table entries of pages that no query sees a key of are not used, so they
+ *     may be -1 (nf_kv_release).  The bytes of keys that no query sees are
+ *     read only where they share a 32-key chunk with seen ones, and take no
+ *     part in the result, whatever they are.
+ *   softmax_scale > 0; max_seqlen <= 2^30.
+ *   All formats and row counts run on the mma.sync kernel (up to 64 rows per
+ *     kv-head, group * n_q).
+ * workspace: at least nf_decode_attn_window_workspace_size(...) bytes, 256-byte
+ *   aligned, zero-filled before its first use; left as nf_decode_attn leaves
+ *   its own, and interchangeable with it.
+ */
+size_t nf_decode_attn_window_workspace_size(int32_t batch, int32_t n_q, int32_t num_q_heads,
+                                            int32_t num_kv_heads, int32_t max_seqlen, int32_t num_sms);
+nf_status nf_decode_attn_window(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch,
+                                int32_t n_q, int32_t num_q_heads, const int32_t *block_table,
+                                int32_t max_blocks, const int32_t *seqlens, int32_t max_seqlen,
+                                int32_t window, int32_t n_sink, float softmax_scale, void *out,
+                                int32_t out_dtype, float *out_lse, void *workspace, size_t workspace_bytes,
+                                nf_stream_t stream);
+
+/*
+ * nf_prefill_attn_window -- nf_prefill_attn with a sliding window and sinks:
+ * the same visibility for the n_q queries of a prompt chunk (or of a whole
+ * prompt, n_q = seqlens[b]).  K8/V4 pool and bf16 q as for nf_prefill_attn;
+ * out of out_dtype, unused rows of length 0, released pages and softmax_scale
+ * > 0 as for nf_decode_attn_window.
+ */
+nf_status nf_prefill_attn_window(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch,
+                                 int32_t n_q, int32_t num_q_heads, const int32_t *block_table,
+                                 int32_t max_blocks, const int32_t *seqlens, int32_t max_seqlen,
+                                 int32_t window, int32_t n_sink, float softmax_scale, void *out,
+                                 int32_t out_dtype, float *out_lse, nf_stream_t stream);
+
+/*
+ * nf_rope_append_quant -- rotary positions on the queries and keys of new
+ * tokens, and nf_kv_append_quant of the turned keys and the values, in one
+ * launch.
+ *
+ * rope: frequency i < rot_dim / 2 turns one pair of channels (x, y) of a
+ *   query or key by the angle a = positions[b][t][axis[i]] * inv_freq[i]:
+ *     (x, y) -> (x cos a - y sin a, y cos a + x sin a),
+ *   the pair being channels (i, i + rot_dim / 2) (NF_ROPE_HALVES) or (2i,
+ *   2i + 1) (NF_ROPE_PAIRS).  Channels from rot_dim on are left as they are.
+ *   One axis is the usual rotary embedding; several axes (time, height, width)
+ *   give image and video tokens their positions.  axis[] may assign the
+ *   frequencies in sections, interleaved or in any other way.  inv_freq: fp32
+ *   [rot_dim / 2], device; rope itself is read before the call returns.
+ * positions: int32 [batch][n_new][n_axes], device; any values (they are not
+ *   the cache positions, which come from seqlens_before as in
+ *   nf_kv_append_quant).
+ * q, k_new, v_new: rows of in_dtype (NF_F32 or NF_BF16), element (b, t, head,
+ *   c) at data + b * batch_stride + t * token_stride + head * 128 + c, so that
+ *   the three parts of a fused projection's output need no copy.  Strides in
+ *   elements, multiples of 4; data 16-byte (NF_F32) or 8-byte (NF_BF16)
+ *   aligned.
+ * q_out: [batch][n_new][num_q_heads][128] of in_dtype; it may be q's own
+ *   memory when q is contiguous.  num_q_heads may be 0 (q and q_out unused).
+ * n_valid: int32 [batch] (device) or NULL: tokens t >= n_valid[b] are padding;
+ *   nothing of them is read, turned or written.
+ * Numerics: angles are exact to about 2^-50 of a turn at any position.  Queries
+ *   are turned in fp32 and rounded once; keys are turned in fp64, rounded to
+ *   fp32 once and then quantised by the pool format's rule (see nf_kv_layer),
+ *   so the pool's bytes are those of this definition.
+ * Errors recorded as by nf_kv_append_quant (q_out is written all the same).
+ * batch * n_new == 0 launches nothing and returns NF_OK.
+ */
+#define NF_ROPE_HALVES 0
+#define NF_ROPE_PAIRS 1
+#define NF_ROPE_MAX_AXES 4
+typedef struct {
+    int32_t rot_dim;  /* channels turned: a multiple of 8 in [8, 128] */
+    int32_t layout;   /* NF_ROPE_HALVES or NF_ROPE_PAIRS */
+    int32_t n_axes;   /* 1 .. NF_ROPE_MAX_AXES */
+    uint8_t axis[64]; /* axis of frequency i, below n_axes, for i < rot_dim / 2 */
+    const float *inv_freq;
+} nf_rope;
+typedef struct {
+    const void *data;
+    int64_t batch_stride, token_stride;
+} nf_heads;
+nf_status nf_rope_append_quant(const nf_kv_layer *kv, const nf_rope *rope, const int32_t *positions,
+                               const nf_heads *q, const nf_heads *k_new, const nf_heads *v_new,
+                               int32_t in_dtype, int32_t batch, int32_t n_new, int32_t num_q_heads,
+                               const int32_t *block_table, int32_t max_blocks,
+                               const int32_t *seqlens_before, const int32_t *n_valid, void *q_out,
+                               nf_stream_t stream);
+
+/*
+ * Pages.  A page is one 256-token block of the pool in every layer; a block
+ * table entry holds its id, or -1 for none.  refs: int32 [num_blocks], device,
+ * owned by the caller and zero at the start: refs[id] is the number of table
+ * entries that hold block id, 0 for a free block.  All decisions are taken on
+ * the device from device memory (the calls can be captured), and none depends
+ * on timing: fresh blocks are the lowest free ids in the order the calls
+ * state.  Calls on one refs / block_table must not overlap on the GPU.
+ * block_table: int32 [rows][max_blocks]; max_blocks <= 2^23, num_blocks <= 2^30.
+ */
+
+/*
+ * nf_kv_reserve -- pages for the positions [from_pos[b], to_pos[b]) of every
+ * row b (int32 [rows], device): each entry of the pages these positions lie in
+ * that is negative gets a fresh block (count 1), in row order and in position
+ * order inside a row; entries that hold a block are left.  from_pos[b] >=
+ * to_pos[b]: nothing.  When the free blocks run out, the entries that come
+ * later in that order stay -1 and NF_DEVERR_POOL is recorded.  A negative from_pos, or
+ * a page index >= max_blocks, is NF_DEVERR_TABLE (that row, those pages).
+ */
+nf_status nf_kv_reserve(int32_t *refs, int32_t num_blocks, int32_t *block_table, int32_t rows,
+                        int32_t max_blocks, const int32_t *from_pos, const int32_t *to_pos,
+                        nf_stream_t stream);
+
+/*
+ * nf_kv_release -- gives up the pages that lie wholly inside [from_pos[b],
+ * to_pos[b]) of every row b: the entry becomes -1 and the block's count goes
+ * down by one (free at 0).  Behind a window: from_pos = n_sink, to_pos = L + 1
+ * - window for the next query at position L.  A whole sequence: from_pos = 0,
+ * to_pos = max_blocks * 256.  Entries of -1 and empty ranges are skipped; a
+ * negative from_pos is NF_DEVERR_TABLE, a block id outside the pool
+ * NF_DEVERR_BLOCK_ID, a count that is not positive NF_DEVERR_REFS (it stays).
+ */
+nf_status nf_kv_release(int32_t *refs, int32_t num_blocks, int32_t *block_table, int32_t rows,
+                        int32_t max_blocks, const int32_t *from_pos, const int32_t *to_pos,
+                        nf_stream_t stream);
+
+/*
+ * nf_kv_copy_blocks -- copies block src[i] to block dst[i] in every plane of
+ * every layer, i < n (int32 [n], device).  src[i] < 0: unused pair; src[i] ==
+ * dst[i]: nothing to do.  A pair whose destination is another used pair's
+ * source or destination is not copied (NF_DEVERR_CONFLICT), nor is one with an
+ * id outside the pool (NF_DEVERR_BLOCK_ID).  layers: n_layers views (host
+ * array, read before the call returns; at most 128) of one format, block count
+ * and head count.
+ */
+nf_status nf_kv_copy_blocks(const nf_kv_layer *layers, int32_t n_layers, const int32_t *src,
+                            const int32_t *dst, int32_t n, nf_stream_t stream);
+
+/* Bytes of device workspace for nf_kv_fork (n_forks pairs) and nf_kv_compact;
+ * it needs no initial contents.  0 for an invalid size. */
+size_t nf_kv_pages_workspace_size(int32_t num_blocks, int32_t n_forks);
+
+/*
+ * nf_kv_fork -- row dst_rows[i] becomes a copy of row src_rows[i], i < n (int32
+ * [n], device; n <= 1024).  With L = seqlens[src]: the L / 256 full pages are
+ * shared (their counts go up); a last page that is partly filled is copied, in
+ * every layer, to a fresh block (handed out in the order of the pairs), so the
+ * two rows then append independently; later entries become -1, and
+ * seqlens[dst] = L.  What the destination row held is released.  One source
+ * may have many destinations; src_rows[i] < 0 is an unused pair.
+ * Not carried out, the destination left as it was: a row index outside the
+ * table (NF_DEVERR_TABLE); a destination that is another used pair's source or
+ * destination, or its own source (NF_DEVERR_CONFLICT); a length outside [0,
+ * max_blocks * 256] (NF_DEVERR_SEQLEN); a partly filled page without a block
+ * (NF_DEVERR_BLOCK_ID); no free block left (NF_DEVERR_POOL).
+ * workspace: nf_kv_pages_workspace_size(num_blocks, n) bytes, 256-byte aligned.
+ */
+nf_status nf_kv_fork(const nf_kv_layer *layers, int32_t n_layers, int32_t *refs, int32_t *block_table,
+                     int32_t rows, int32_t max_blocks, const int32_t *src_rows, const int32_t *dst_rows,
+                     int32_t n, int32_t *seqlens, void *workspace, size_t workspace_bytes,
+                     nf_stream_t stream);
+
+/*
+ * nf_kv_compact -- moves the blocks in use to the front of the pool: with n of
+ * them, the i-th (by id) that lies at n or behind goes to the i-th free block
+ * before n, in every layer; counts and table entries follow, and every block
+ * from n on is free.  Ids held anywhere but in this table become invalid.
+ * A table entry whose block no count stands for becomes -1 when it lies at n
+ * or behind (NF_DEVERR_REFS).
+ * workspace: nf_kv_pages_workspace_size(num_blocks, 0) bytes, 256-byte aligned.
+ */
+nf_status nf_kv_compact(const nf_kv_layer *layers, int32_t n_layers, int32_t *refs, int32_t *block_table,
+                        int32_t rows, int32_t max_blocks, void *workspace, size_t workspace_bytes,
+                        nf_stream_t stream);
 
 /*
  * nf_get_device_error -- read and clear the device error code of the current

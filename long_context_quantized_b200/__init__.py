@@ -19,6 +19,10 @@ __all__ = [
     "NF_OK", "NF_KV_K8V4", "NF_KV_BF16", "NF_KV_K8V8", "NF_KV_F8", "NF_KV_K4V4", "NF_F32", "NF_BF16", "NfError", "KVLayer",
     "nf_kv_append_quant", "nf_decode_attn_workspace_size", "nf_decode_attn", "nf_decode_attn_noalloc",
     "nf_attn_combine", "nf_attn_packed_slot_floats", "nf_attn_combine_packed", "nf_prefill_attn",
+    "nf_decode_attn_window", "nf_decode_attn_window_workspace_size", "nf_prefill_attn_window",
+    "Rope", "NF_ROPE_HALVES", "NF_ROPE_PAIRS", "nf_rope_append_quant",
+    "KVLayers", "nf_kv_reserve", "nf_kv_release", "nf_kv_copy_blocks", "nf_kv_pages_workspace_size", "nf_kv_fork",
+    "nf_kv_compact",
     "nf_get_device_error", "nf_status_string", "library_path", "load_library",
 ]
 
@@ -31,6 +35,8 @@ NF_OK = 0
 NF_ERR_INVALID_ARG, NF_ERR_UNSUPPORTED, NF_ERR_WORKSPACE, NF_ERR_CUDA, NF_ERR_DEVICE_CHECK = 1, 2, 3, 4, 5
 NF_DEVERR_NONE, NF_DEVERR_BLOCK_ID, NF_DEVERR_TABLE, NF_DEVERR_SEQLEN = 0, 1, 2, 3
 NF_DEVERR_TIMEOUT, NF_DEVERR_INTERNAL, NF_DEVERR_RANGE = 4, 5, 6
+NF_DEVERR_CONFLICT, NF_DEVERR_POOL, NF_DEVERR_REFS = 7, 8, 9
+NF_ROPE_HALVES, NF_ROPE_PAIRS, NF_ROPE_MAX_AXES = 0, 1, 4
 NF_F32, NF_BF16, NF_F16 = 0, 1, 2
 NF_KV_K8V4, NF_KV_BF16, NF_KV_K8V8, NF_KV_F8, NF_KV_K4V4 = 0, 1, 2, 3, 4
 BLOCK = 256
@@ -50,6 +56,15 @@ class nf_kv_layer(ctypes.Structure):
         ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
         ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
     ]
+
+
+class nf_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 64), ("inv_freq", ctypes.c_void_p)]
+
+
+class nf_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -92,6 +107,25 @@ def load_library():
         lib.nf_attn_packed_slot_floats.restype = S
         lib.nf_attn_combine_packed.argtypes = [P, I, I, I, P, P, P]
         lib.nf_attn_combine_packed.restype = I
+        F = ctypes.c_float
+        lib.nf_decode_attn_window_workspace_size.argtypes = [I, I, I, I, I, I]
+        lib.nf_decode_attn_window_workspace_size.restype = S
+        lib.nf_decode_attn_window.argtypes = [P, P, I, I, I, I, P, I, P, I, I, I, F, P, I, P, P, S, P]
+        lib.nf_decode_attn_window.restype = I
+        lib.nf_prefill_attn_window.argtypes = [P, P, I, I, I, I, P, I, P, I, I, I, F, P, I, P, P]
+        lib.nf_prefill_attn_window.restype = I
+        lib.nf_rope_append_quant.argtypes = [P, P, P, P, P, P, I, I, I, I, P, I, P, P, P, P]
+        lib.nf_rope_append_quant.restype = I
+        lib.nf_kv_reserve.argtypes = lib.nf_kv_release.argtypes = [P, I, P, I, I, P, P, P]
+        lib.nf_kv_reserve.restype = lib.nf_kv_release.restype = I
+        lib.nf_kv_copy_blocks.argtypes = [P, I, P, P, I, P]
+        lib.nf_kv_copy_blocks.restype = I
+        lib.nf_kv_pages_workspace_size.argtypes = [I, I]
+        lib.nf_kv_pages_workspace_size.restype = S
+        lib.nf_kv_fork.argtypes = [P, I, P, P, I, I, P, P, I, P, P, S, P]
+        lib.nf_kv_fork.restype = I
+        lib.nf_kv_compact.argtypes = [P, I, P, P, I, I, P, S, P]
+        lib.nf_kv_compact.restype = I
         lib.nf_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int32)]
         lib.nf_get_device_error.restype = I
         lib.nf_status_string.argtypes = [I]
@@ -155,6 +189,7 @@ class KVLayer:
         self.c = nf_kv_layer(fmt, self.num_blocks, BLOCK, self.num_kv_heads, HEAD_DIM, 32,
                              k_codes.data_ptr(), 0 if k_scales is None else k_scales.data_ptr(),
                              v_codes.data_ptr(), 0 if v_scales is None else v_scales.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, fmt: int, num_blocks: int, num_kv_heads: int, device="cuda", fill: int | None = None):
@@ -337,3 +372,239 @@ def nf_selftest_bounded_wait(limit_us: int, stream=None):
     """Run the bounded-wait self-test (see nf.h); afterwards
     nf_get_device_error() returns NF_DEVERR_TIMEOUT."""
     _check(load_library().nf_selftest_bounded_wait(int(limit_us), _stream(stream)), "nf_selftest_bounded_wait")
+
+
+# ---------------------------------------------------------------- windowed sessions
+def _refuse(where, message):
+    raise NfError(NF_ERR_INVALID_ARG, where, message)
+
+
+def _same_device(where, device, **tensors):
+    """Every tensor contiguous, of its dtype, on `device`, which is the current one."""
+    if device.type != "cuda":
+        _refuse(where, "tensors must be on a CUDA device")
+    if device.index != torch.cuda.current_device():
+        _refuse(where, f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            _refuse(where, f"{name} is on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            _refuse(where, f"{name} must be contiguous")
+        if t.dtype != dtype:
+            _refuse(where, f"{name}: dtype {t.dtype}, expected {dtype}")
+
+
+def nf_decode_attn_window_workspace_size(batch, n_q, num_q_heads, num_kv_heads, max_seqlen, num_sms=None):
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return int(load_library().nf_decode_attn_window_workspace_size(batch, n_q, num_q_heads, num_kv_heads, max_seqlen,
+                                                                   num_sms))
+
+
+def _window_args(where, kv, q, block_table, seqlens, out, out_lse):
+    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
+        _refuse(where, "q must be [batch][n_q][H_q][128]")
+    _same_device(where, q.device, q=(q, q.dtype), block_table=(block_table, torch.int32),
+                 seqlens=(seqlens, torch.int32), out=(out, out.dtype), out_lse=(out_lse, torch.float32))
+    if kv.k_codes.device != q.device:
+        _refuse(where, f"the pool is on {kv.k_codes.device}, q on {q.device}")
+    if out.shape != q.shape:
+        _refuse(where, "out must have q's shape")
+    if out_lse is not None and out_lse.shape != q.shape[:3]:
+        _refuse(where, "out_lse must be [batch][n_q][H_q]")
+    if block_table.dim() != 2 or block_table.shape[0] != q.shape[0] or seqlens.shape != q.shape[:1]:
+        _refuse(where, "block_table [batch][max_blocks] and seqlens [batch] must have q's batch")
+
+
+def nf_decode_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int, window: int, n_sink: int,
+                          softmax_scale: float, out, out_lse=None, workspace=None, stream=None):
+    """Decode attention with a sliding window and sinks: a query at position P
+    sees the keys t <= P with t > P - window or t < n_sink (see nf.h).  out
+    (fp32 or bf16) has the shape of q [batch][n_q][H_q][128]; seqlens 0 marks an
+    unused row of the batch."""
+    _window_args("nf_decode_attn_window", kv, q, block_table, seqlens, out, out_lse)
+    if workspace is None:
+        raise NfError(NF_ERR_WORKSPACE, "nf_decode_attn_window", "workspace tensor required "
+                      "(size: nf_decode_attn_window_workspace_size)")
+    _same_device("nf_decode_attn_window", q.device, workspace=(workspace, workspace.dtype))
+    B, n_q, H_q, _ = q.shape
+    st = load_library().nf_decode_attn_window(
+        kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1],
+        seqlens.data_ptr(), max_seqlen, window, n_sink, softmax_scale, out.data_ptr(), _dtype_code(out.dtype),
+        None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _check(st, "nf_decode_attn_window")
+
+
+def nf_prefill_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int, window: int, n_sink: int,
+                           softmax_scale: float, out, out_lse=None, stream=None):
+    """Chunked-prefill attention with a sliding window and sinks (see nf.h and
+    nf_decode_attn_window): bf16 q over a K8/V4 pool, out fp32 or bf16."""
+    _window_args("nf_prefill_attn_window", kv, q, block_table, seqlens, out, out_lse)
+    B, n_q, H_q, _ = q.shape
+    st = load_library().nf_prefill_attn_window(
+        kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1],
+        seqlens.data_ptr(), max_seqlen, window, n_sink, softmax_scale, out.data_ptr(), _dtype_code(out.dtype),
+        None if out_lse is None else out_lse.data_ptr(), _stream(stream))
+    _check(st, "nf_prefill_attn_window")
+
+
+class Rope:
+    """The rotary frequencies of a model: ``inv_freq`` (fp32 [rot_dim / 2],
+    device), the position axis of each frequency (``axis``, a sequence of
+    rot_dim / 2 numbers below ``n_axes``; None: axis 0 for all) and the layout
+    of the channel pairs (see nf_rope in nf.h)."""
+
+    def __init__(self, inv_freq, axis=None, n_axes: int = 1, layout: int = NF_ROPE_HALVES):
+        _need(inv_freq, "inv_freq", torch.float32)
+        half = inv_freq.numel()
+        axis = [0] * half if axis is None else [int(a) for a in axis]
+        if len(axis) != half or half > 64 or any(not 0 <= a < n_axes for a in axis):
+            _refuse("Rope", "axis must hold one axis below n_axes for each of the (at most 64) frequencies")
+        self.inv_freq, self.n_axes = inv_freq, int(n_axes)
+        self.c = nf_rope(2 * half, layout, n_axes, (ctypes.c_uint8 * 64)(*axis), inv_freq.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+
+def _heads(where, name, t, dtype, device, batch, n_new):
+    if t.dim() != 4 or t.shape[0] != batch or t.shape[1] != n_new or t.shape[3] != HEAD_DIM:
+        _refuse(where, f"{name} must be [batch][n_new][heads][128]")
+    if t.dtype != dtype or t.device != device:
+        _refuse(where, f"{name}: {t.dtype} on {t.device}, expected {dtype} on {device}")
+    sb, st, sh, sc = t.stride()
+    if (sc != 1 or (sh != HEAD_DIM and t.shape[2] > 1)) and t.numel():
+        _refuse(where, f"{name}: the heads of a token must be contiguous")
+    return nf_heads(t.data_ptr(), sb, st)
+
+
+def nf_rope_append_quant(kv: KVLayer, rope: Rope, positions, q, k_new, v_new, block_table, seqlens_before, q_out,
+                         n_valid=None, stream=None):
+    """Turn q and k_new by the rotary angles of ``positions`` (int32
+    [batch][n_new][n_axes]), write q_out, and quantise the turned keys and the
+    values into the pool at seqlens_before[b] + i (see nf.h).  q [batch][n_new]
+    [H_q][128], k_new and v_new [batch][n_new][H_kv][128] of one dtype may be
+    strided views (of a fused projection's output) whose heads are contiguous;
+    tokens from n_valid[b] on are padding.  q and q_out may be None."""
+    where = "nf_rope_append_quant"
+    B, n_new = k_new.shape[0], k_new.shape[1]
+    dtype, device = k_new.dtype, k_new.device
+    k = _heads(where, "k_new", k_new, dtype, device, B, n_new)
+    v = _heads(where, "v_new", v_new, dtype, device, B, n_new)
+    if k_new.shape[2] != kv.num_kv_heads or v_new.shape[2] != kv.num_kv_heads:
+        _refuse(where, f"k_new / v_new must have the pool's {kv.num_kv_heads} heads")
+    H_q = 0
+    qh = nf_heads(None, 0, 0)
+    if q is not None:
+        qh = _heads(where, "q", q, dtype, device, B, n_new)
+        H_q = q.shape[2]
+        if q_out is None or q_out.shape != q.shape:
+            _refuse(where, "q_out must have q's shape")
+    _same_device(where, device, positions=(positions, torch.int32), block_table=(block_table, torch.int32),
+                 seqlens_before=(seqlens_before, torch.int32), n_valid=(n_valid, torch.int32), q_out=(q_out, dtype))
+    if kv.k_codes.device != device or rope.inv_freq.device != device:
+        _refuse(where, "the pool, inv_freq and the inputs must be on one device")
+    if positions.shape != (B, n_new, rope.n_axes):
+        _refuse(where, f"positions must be [batch][n_new][{rope.n_axes}]")
+    if (block_table.dim() != 2 or block_table.shape[0] != B or seqlens_before.shape != (B,)
+            or (n_valid is not None and n_valid.shape != (B,))):
+        _refuse(where, "block_table, seqlens_before and n_valid must have the inputs' batch")
+    st = load_library().nf_rope_append_quant(
+        kv.ref, rope.ref, positions.data_ptr(), ctypes.byref(qh), ctypes.byref(k), ctypes.byref(v), _dtype_code(dtype),
+        B, n_new, H_q, block_table.data_ptr(), block_table.shape[1], seqlens_before.data_ptr(),
+        None if n_valid is None else n_valid.data_ptr(), None if q_out is None else q_out.data_ptr(), _stream(stream))
+    _check(st, where)
+
+
+class KVLayers:
+    """The layers of one pool (KVLayer views of one format, block count and
+    head count), for the page calls that move blocks in all of them."""
+
+    def __init__(self, layers):
+        self.layers = list(layers)
+        if not self.layers:
+            _refuse("KVLayers", "no layers")
+        self.num_blocks = self.layers[0].num_blocks
+        self.device = self.layers[0].k_codes.device
+        if any(layer.k_codes.device != self.device for layer in self.layers):
+            _refuse("KVLayers", "the layers must be on one device")
+        self.c = (nf_kv_layer * len(self.layers))(*[layer.c for layer in self.layers])
+
+    def __len__(self):
+        return len(self.layers)
+
+
+def _pages_args(where, refs, block_table, rows_of=(), **more):
+    _same_device(where, refs.device, refs=(refs, torch.int32), block_table=(block_table, torch.int32), **more)
+    if refs.dim() != 1 or block_table.dim() != 2:
+        _refuse(where, "refs must be [num_blocks], block_table [rows][max_blocks]")
+    for name in rows_of:
+        if more[name][0].shape != block_table.shape[:1]:
+            _refuse(where, f"{name} must be [rows]")
+
+
+def _range_call(where, refs, block_table, from_pos, to_pos, stream):
+    _pages_args(where, refs, block_table, ("from_pos", "to_pos"), from_pos=(from_pos, torch.int32),
+                to_pos=(to_pos, torch.int32))
+    st = getattr(load_library(), where)(refs.data_ptr(), refs.shape[0], block_table.data_ptr(), block_table.shape[0],
+                                        block_table.shape[1], from_pos.data_ptr(), to_pos.data_ptr(), _stream(stream))
+    _check(st, where)
+
+
+def nf_kv_reserve(refs, block_table, from_pos, to_pos, stream=None):
+    """Fresh pages for the positions [from_pos[b], to_pos[b]) of every table
+    row that have none (see nf.h): the lowest free blocks, in row order."""
+    _range_call("nf_kv_reserve", refs, block_table, from_pos, to_pos, stream)
+
+
+def nf_kv_release(refs, block_table, from_pos, to_pos, stream=None):
+    """Give up the pages wholly inside [from_pos[b], to_pos[b]) of every table
+    row (see nf.h): behind a window, or a whole sequence."""
+    _range_call("nf_kv_release", refs, block_table, from_pos, to_pos, stream)
+
+
+def nf_kv_copy_blocks(layers: KVLayers, src, dst, stream=None):
+    """Copy block src[i] to dst[i] in every layer (int32 [n]; see nf.h)."""
+    where = "nf_kv_copy_blocks"
+    _same_device(where, layers.device, src=(src, torch.int32), dst=(dst, torch.int32))
+    if src.dim() != 1 or src.shape != dst.shape:
+        _refuse(where, "src and dst must be [n]")
+    st = load_library().nf_kv_copy_blocks(layers.c, len(layers), src.data_ptr(), dst.data_ptr(), src.shape[0],
+                                          _stream(stream))
+    _check(st, where)
+
+
+def nf_kv_pages_workspace_size(num_blocks: int, n_forks: int = 0) -> int:
+    """Bytes of workspace of nf_kv_fork (n_forks pairs) and nf_kv_compact."""
+    return int(load_library().nf_kv_pages_workspace_size(num_blocks, n_forks))
+
+
+def nf_kv_fork(layers: KVLayers, refs, block_table, src_rows, dst_rows, seqlens, workspace, stream=None):
+    """Make table row dst_rows[i] a copy of row src_rows[i] (see nf.h): full
+    pages are shared, a partly filled last page is copied in every layer, and
+    seqlens[dst] = seqlens[src]."""
+    where = "nf_kv_fork"
+    _pages_args(where, refs, block_table, ("seqlens",), src_rows=(src_rows, torch.int32),
+                dst_rows=(dst_rows, torch.int32), seqlens=(seqlens, torch.int32), workspace=(workspace, workspace.dtype))
+    if refs.shape[0] != layers.num_blocks or layers.device != refs.device:
+        _refuse(where, "refs must have one count per block of the pool, on its device")
+    if src_rows.dim() != 1 or src_rows.shape != dst_rows.shape:
+        _refuse(where, "src_rows and dst_rows must be [n]")
+    st = load_library().nf_kv_fork(
+        layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
+        src_rows.data_ptr(), dst_rows.data_ptr(), src_rows.shape[0], seqlens.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, _stream(stream))
+    _check(st, where)
+
+
+def nf_kv_compact(layers: KVLayers, refs, block_table, workspace, stream=None):
+    """Move the blocks in use to the front of the pool, in every layer, and
+    renumber the table (see nf.h)."""
+    where = "nf_kv_compact"
+    _pages_args(where, refs, block_table, workspace=(workspace, workspace.dtype))
+    if refs.shape[0] != layers.num_blocks or layers.device != refs.device:
+        _refuse(where, "refs must have one count per block of the pool, on its device")
+    st = load_library().nf_kv_compact(
+        layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
+        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _check(st, where)

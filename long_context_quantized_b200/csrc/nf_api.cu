@@ -15,7 +15,9 @@
 #include "nf_common.cuh"
 #include "nf_decode.cuh"
 #include "nf_decode_tc.cuh"
+#include "nf_pages.cuh"
 #include "nf_prefill.cuh"
+#include "nf_rope.cuh"
 
 namespace nf {
 // Self-test of the bounded wait: one thread waits on an mbarrier that nothing
@@ -174,7 +176,7 @@ cudaError_t launch_pdl(Kern kernel, unsigned grid, unsigned block, size_t smem, 
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int NT, bool QF32, int FMT>
+template <int NT, bool QF32, int FMT, bool WIN>
 cudaError_t launch_decode(const nf::DecodeParams &p, int ctas, cudaStream_t s) {
     constexpr int smem = nf::DecodeSmem<NT, FMT>::kBytes;
     // opt in to the large dynamic shared memory, once per device
@@ -184,11 +186,11 @@ cudaError_t launch_decode(const nf::DecodeParams &p, int ctas, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(opted.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(nf::decode_kernel<NT, QF32, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(nf::decode_kernel<NT, QF32, FMT, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         opted.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_pdl(nf::decode_kernel<NT, QF32, FMT>, (unsigned)ctas, nf::kDecodeThreads, smem, s, p);
+    return launch_pdl(nf::decode_kernel<NT, QF32, FMT, WIN>, (unsigned)ctas, nf::kDecodeThreads, smem, s, p);
 }
 
 // The tensor-core decode of many rows (K8/V4 or K8V8, 9 to 32 query rows per
@@ -218,17 +220,17 @@ bool uses_decode_tc(int fmt, int rows) {
     return (fmt == NF_KV_K8V4 || fmt == NF_KV_K8V8 || fmt == NF_KV_F8) && rows > 8 && rows <= nf::kDtMaxRows;
 }
 
-template <int NT>
+template <int NT, bool WIN, int FMT>
+cudaError_t dispatch_decode_q(const nf::DecodeParams &p, bool qf32, int ctas, cudaStream_t s) {
+    return qf32 ? launch_decode<NT, true, FMT, WIN>(p, ctas, s) : launch_decode<NT, false, FMT, WIN>(p, ctas, s);
+}
+template <int NT, bool WIN>
 cudaError_t dispatch_decode(const nf::DecodeParams &p, bool qf32, int fmt, int ctas, cudaStream_t s) {
-    if (fmt == NF_KV_K8V4)
-        return qf32 ? launch_decode<NT, true, NF_KV_K8V4>(p, ctas, s) : launch_decode<NT, false, NF_KV_K8V4>(p, ctas, s);
-    if (fmt == NF_KV_K8V8)
-        return qf32 ? launch_decode<NT, true, NF_KV_K8V8>(p, ctas, s) : launch_decode<NT, false, NF_KV_K8V8>(p, ctas, s);
-    if (fmt == NF_KV_F8)
-        return qf32 ? launch_decode<NT, true, NF_KV_F8>(p, ctas, s) : launch_decode<NT, false, NF_KV_F8>(p, ctas, s);
-    if (fmt == NF_KV_K4V4)
-        return qf32 ? launch_decode<NT, true, NF_KV_K4V4>(p, ctas, s) : launch_decode<NT, false, NF_KV_K4V4>(p, ctas, s);
-    return qf32 ? launch_decode<NT, true, NF_KV_BF16>(p, ctas, s) : launch_decode<NT, false, NF_KV_BF16>(p, ctas, s);
+    if (fmt == NF_KV_K8V4) return dispatch_decode_q<NT, WIN, NF_KV_K8V4>(p, qf32, ctas, s);
+    if (fmt == NF_KV_K8V8) return dispatch_decode_q<NT, WIN, NF_KV_K8V8>(p, qf32, ctas, s);
+    if (fmt == NF_KV_F8) return dispatch_decode_q<NT, WIN, NF_KV_F8>(p, qf32, ctas, s);
+    if (fmt == NF_KV_K4V4) return dispatch_decode_q<NT, WIN, NF_KV_K4V4>(p, qf32, ctas, s);
+    return dispatch_decode_q<NT, WIN, NF_KV_BF16>(p, qf32, ctas, s);
 }
 
 nf_status launch_combine(const float *part_o, const float *part_lse, int n_splits, int rows,
@@ -268,6 +270,136 @@ nf_status noalloc_scratch(void **ptr) {
     }
     *ptr = g_noalloc_ptr[dev];
     return NF_OK;
+}
+
+// The window of a windowed attention call, checked; window and n_sink are cut
+// to max_seqlen, beyond which they change nothing (and no sum of positions can
+// overflow).
+struct Window {
+    int window, n_sink, out_bf16;
+};
+constexpr int kMaxWindowSeqlen = 1 << 30;
+nf_status check_window(int window, int n_sink, int max_seqlen, float softmax_scale, int out_dtype, Window &w) {
+    if (window < 1) return fail(NF_ERR_INVALID_ARG, "window %d < 1", window);
+    if (n_sink < 0) return fail(NF_ERR_INVALID_ARG, "n_sink %d < 0", n_sink);
+    if (max_seqlen > kMaxWindowSeqlen)
+        return fail(NF_ERR_UNSUPPORTED, "max_seqlen %d above %d", max_seqlen, kMaxWindowSeqlen);
+    if (!(softmax_scale > 0.f)) return fail(NF_ERR_INVALID_ARG, "softmax_scale must be positive");
+    if (out_dtype != NF_F32 && out_dtype != NF_BF16)
+        return fail(NF_ERR_UNSUPPORTED, "out_dtype %d (NF_F32 or NF_BF16)", out_dtype);
+    w.window = window < max_seqlen ? window : max_seqlen;
+    w.n_sink = n_sink < max_seqlen ? n_sink : max_seqlen;
+    w.out_bf16 = out_dtype == NF_BF16;
+    return NF_OK;
+}
+
+// nf_decode_attn_ex and (win != nullptr) nf_decode_attn_window.
+nf_status run_decode(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch, int32_t n_q,
+                     int32_t num_q_heads, const int32_t *block_table, int32_t max_blocks, const int32_t *seqlens,
+                     int32_t max_seqlen, float softmax_scale, int32_t causal, uint32_t flags, const Window *win,
+                     void *out, float *out_lse, void *workspace, size_t workspace_bytes, nf_stream_t stream) {
+    nf_status st = check_layer(kv);
+    if (st != NF_OK) return st;
+    if (q_dtype != NF_F32 && q_dtype != NF_BF16)
+        return fail(NF_ERR_UNSUPPORTED, "q_dtype %d (NF_F32 or NF_BF16)", q_dtype);
+    if (batch < 1 || n_q < 1 || num_q_heads < 1)
+        return fail(NF_ERR_INVALID_ARG, "batch %d, n_q %d, num_q_heads %d must be >= 1", batch, n_q,
+                    num_q_heads);
+    if (batch > 65535 || kv->num_kv_heads > 65535)
+        return fail(NF_ERR_UNSUPPORTED, "batch %d / num_kv_heads %d above 65535", batch, kv->num_kv_heads);
+    if (num_q_heads % kv->num_kv_heads != 0)
+        return fail(NF_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d",
+                    num_q_heads, kv->num_kv_heads);
+    if (max_seqlen < n_q) return fail(NF_ERR_INVALID_ARG, "max_seqlen %d < n_q %d", max_seqlen, n_q);
+    if ((long long)max_blocks * nf::kBlock < max_seqlen)
+        return fail(NF_ERR_INVALID_ARG, "max_blocks %d cannot hold max_seqlen %d", max_blocks, max_seqlen);
+    if (!q || !block_table || !seqlens || !out) return fail(NF_ERR_INVALID_ARG, "a device pointer is NULL");
+    if (!std::isfinite(softmax_scale)) return fail(NF_ERR_INVALID_ARG, "softmax_scale is not finite");
+    const uintptr_t qa = reinterpret_cast<uintptr_t>(q);
+    if ((q_dtype == NF_F32 && (qa & 15)) || (q_dtype == NF_BF16 && (qa & 7)) ||
+        (reinterpret_cast<uintptr_t>(out) & 15))
+        return fail(NF_ERR_INVALID_ARG, "q / out misaligned");
+    const int sms = current_sm_count();
+    if (sms < 1) return fail(NF_ERR_CUDA, "cannot query the current device");
+    Plan pl;
+    if (!make_plan(batch, n_q, num_q_heads, kv->num_kv_heads, max_seqlen, sms, pl))
+        return fail(NF_ERR_UNSUPPORTED, "unsupported shape (batch <= %d and group * n_q <= %d)", nf::kMaxBatch,
+                    nf::kMaxRows);
+    if (workspace_bytes < pl.bytes() || !workspace)
+        return fail(NF_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes());
+    if (reinterpret_cast<uintptr_t>(workspace) & 255)
+        return fail(NF_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+
+    nf::DecodeParams p{};
+    const bool tc = !win && uses_decode_tc(kv->fmt, pl.rows);
+    // decode_tc_kernel loads a tile's K and V rows with one box each
+    const unsigned box_rows = tc ? (unsigned)nf::kDtTileKeys : (unsigned)nf::kChunk;
+    if (kv->fmt != NF_KV_BF16) {
+        st = encode_v_map(kv, &p.vmap, false, box_rows);
+        if (st != NF_OK) return st;
+    }
+    if (tc || kv->fmt == NF_KV_K4V4) {
+        st = encode_v_map(kv, &p.kmap, true, box_rows);
+        if (st != NF_OK) return st;
+    }
+    if (!tc && kv->fmt != NF_KV_BF16) {
+        // decode_kernel: a whole stage's V (and RK4V4 K) rows in one box
+        const unsigned stage_rows = (kv->fmt == NF_KV_K8V8 || kv->fmt == NF_KV_F8) ? 128u : 256u;
+        st = encode_v_map(kv, &p.vmap_full, false, stage_rows);
+        if (st != NF_OK) return st;
+        if (kv->fmt == NF_KV_K4V4) {
+            st = encode_v_map(kv, &p.kmap_full, true, stage_rows);
+            if (st != NF_OK) return st;
+        }
+    }
+    p.k_codes = kv->k_codes;
+    p.k_scales = static_cast<const __half *>(kv->k_scales);
+    p.v_codes = kv->v_codes;
+    p.v_scales = static_cast<const __half *>(kv->v_scales);
+    p.num_blocks = kv->num_blocks;
+    p.num_kv_heads = kv->num_kv_heads;
+    p.q = q;
+    p.batch = batch;
+    p.n_q = n_q;
+    p.num_q_heads = num_q_heads;
+    p.group = num_q_heads / kv->num_kv_heads;
+    p.rows = pl.rows;
+    p.n_rg = pl.n_rg;
+    p.block_table = block_table;
+    p.max_blocks = max_blocks;
+    p.seqlens = seqlens;
+    p.max_seqlen = max_seqlen;
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.causal = causal != 0;
+    p.early_kv = (flags & NF_DECODE_EARLY_KV) != 0;
+    p.out = static_cast<float *>(out);
+    p.out_lse = out_lse;
+    p.tickets = static_cast<int32_t *>(workspace);
+    p.done = p.tickets + pl.segments;
+    p.claims = p.done + pl.segments;
+    p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.ticket_bytes);
+    p.slot_floats = pl.slot_floats;
+    if (win) {
+        p.window = win->window;
+        p.n_sink = win->n_sink;
+        p.out_bf16 = win->out_bf16;
+    }
+
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool qf32 = q_dtype == NF_F32;
+    const cudaError_t e =
+        tc ? (kv->fmt == NF_KV_K8V8 ? dispatch_decode_tc<NF_KV_K8V8>(p, qf32, pl.rows, pl.ctas, s)
+              : kv->fmt == NF_KV_F8 ? dispatch_decode_tc<NF_KV_F8>(p, qf32, pl.rows, pl.ctas, s)
+                                    : dispatch_decode_tc<NF_KV_K8V4>(p, qf32, pl.rows, pl.ctas, s))
+        : win ? (pl.nt == 1 ? dispatch_decode<1, true>(p, qf32, kv->fmt, pl.ctas, s)
+                            : dispatch_decode<2, true>(p, qf32, kv->fmt, pl.ctas, s))
+              : (pl.nt == 1 ? dispatch_decode<1, false>(p, qf32, kv->fmt, pl.ctas, s)
+                            : dispatch_decode<2, false>(p, qf32, kv->fmt, pl.ctas, s));
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(NF_ERR_CUDA, "decode kernel set-up: %s", cudaGetErrorString(e));
+    }
+    return after_launch("decode kernel launch");
 }
 
 }  // namespace
@@ -341,101 +473,8 @@ nf_status nf_decode_attn_ex(const nf_kv_layer *kv, const void *q, int32_t q_dtyp
                             float softmax_scale, int32_t causal, uint32_t flags, float *out,
                             float *out_lse, void *workspace, size_t workspace_bytes, nf_stream_t stream) {
     if (flags & ~NF_DECODE_EARLY_KV) return fail(NF_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
-    nf_status st = check_layer(kv);
-    if (st != NF_OK) return st;
-    if (q_dtype != NF_F32 && q_dtype != NF_BF16)
-        return fail(NF_ERR_UNSUPPORTED, "q_dtype %d (NF_F32 or NF_BF16)", q_dtype);
-    if (batch < 1 || n_q < 1 || num_q_heads < 1)
-        return fail(NF_ERR_INVALID_ARG, "batch %d, n_q %d, num_q_heads %d must be >= 1", batch, n_q,
-                    num_q_heads);
-    if (batch > 65535 || kv->num_kv_heads > 65535)
-        return fail(NF_ERR_UNSUPPORTED, "batch %d / num_kv_heads %d above 65535", batch, kv->num_kv_heads);
-    if (num_q_heads % kv->num_kv_heads != 0)
-        return fail(NF_ERR_INVALID_ARG, "num_q_heads %d not a multiple of num_kv_heads %d",
-                    num_q_heads, kv->num_kv_heads);
-    if (max_seqlen < n_q) return fail(NF_ERR_INVALID_ARG, "max_seqlen %d < n_q %d", max_seqlen, n_q);
-    if ((long long)max_blocks * nf::kBlock < max_seqlen)
-        return fail(NF_ERR_INVALID_ARG, "max_blocks %d cannot hold max_seqlen %d", max_blocks, max_seqlen);
-    if (!q || !block_table || !seqlens || !out) return fail(NF_ERR_INVALID_ARG, "a device pointer is NULL");
-    if (!std::isfinite(softmax_scale)) return fail(NF_ERR_INVALID_ARG, "softmax_scale is not finite");
-    const uintptr_t qa = reinterpret_cast<uintptr_t>(q);
-    if ((q_dtype == NF_F32 && (qa & 15)) || (q_dtype == NF_BF16 && (qa & 7)) ||
-        (reinterpret_cast<uintptr_t>(out) & 15))
-        return fail(NF_ERR_INVALID_ARG, "q / out misaligned");
-    const int sms = current_sm_count();
-    if (sms < 1) return fail(NF_ERR_CUDA, "cannot query the current device");
-    Plan pl;
-    if (!make_plan(batch, n_q, num_q_heads, kv->num_kv_heads, max_seqlen, sms, pl))
-        return fail(NF_ERR_UNSUPPORTED, "unsupported shape (batch <= %d and group * n_q <= %d)", nf::kMaxBatch,
-                    nf::kMaxRows);
-    if (workspace_bytes < pl.bytes() || !workspace)
-        return fail(NF_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, pl.bytes());
-    if (reinterpret_cast<uintptr_t>(workspace) & 255)
-        return fail(NF_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-
-    nf::DecodeParams p{};
-    const bool tc = uses_decode_tc(kv->fmt, pl.rows);
-    // decode_tc_kernel loads a tile's K and V rows with one box each
-    const unsigned box_rows = tc ? (unsigned)nf::kDtTileKeys : (unsigned)nf::kChunk;
-    if (kv->fmt != NF_KV_BF16) {
-        st = encode_v_map(kv, &p.vmap, false, box_rows);
-        if (st != NF_OK) return st;
-    }
-    if (tc || kv->fmt == NF_KV_K4V4) {
-        st = encode_v_map(kv, &p.kmap, true, box_rows);
-        if (st != NF_OK) return st;
-    }
-    if (!tc && kv->fmt != NF_KV_BF16) {
-        // decode_kernel: a whole stage's V (and RK4V4 K) rows in one box
-        const unsigned stage_rows = (kv->fmt == NF_KV_K8V8 || kv->fmt == NF_KV_F8) ? 128u : 256u;
-        st = encode_v_map(kv, &p.vmap_full, false, stage_rows);
-        if (st != NF_OK) return st;
-        if (kv->fmt == NF_KV_K4V4) {
-            st = encode_v_map(kv, &p.kmap_full, true, stage_rows);
-            if (st != NF_OK) return st;
-        }
-    }
-    p.k_codes = kv->k_codes;
-    p.k_scales = static_cast<const __half *>(kv->k_scales);
-    p.v_codes = kv->v_codes;
-    p.v_scales = static_cast<const __half *>(kv->v_scales);
-    p.num_blocks = kv->num_blocks;
-    p.num_kv_heads = kv->num_kv_heads;
-    p.q = q;
-    p.batch = batch;
-    p.n_q = n_q;
-    p.num_q_heads = num_q_heads;
-    p.group = num_q_heads / kv->num_kv_heads;
-    p.rows = pl.rows;
-    p.n_rg = pl.n_rg;
-    p.block_table = block_table;
-    p.max_blocks = max_blocks;
-    p.seqlens = seqlens;
-    p.max_seqlen = max_seqlen;
-    p.scale_log2 = softmax_scale * 1.4426950408889634f;
-    p.causal = causal != 0;
-    p.early_kv = (flags & NF_DECODE_EARLY_KV) != 0;
-    p.out = out;
-    p.out_lse = out_lse;
-    p.tickets = static_cast<int32_t *>(workspace);
-    p.done = p.tickets + pl.segments;
-    p.claims = p.done + pl.segments;
-    p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.ticket_bytes);
-    p.slot_floats = pl.slot_floats;
-
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool qf32 = q_dtype == NF_F32;
-    const cudaError_t e =
-        tc ? (kv->fmt == NF_KV_K8V8 ? dispatch_decode_tc<NF_KV_K8V8>(p, qf32, pl.rows, pl.ctas, s)
-              : kv->fmt == NF_KV_F8 ? dispatch_decode_tc<NF_KV_F8>(p, qf32, pl.rows, pl.ctas, s)
-                                    : dispatch_decode_tc<NF_KV_K8V4>(p, qf32, pl.rows, pl.ctas, s))
-        : pl.nt == 1 ? dispatch_decode<1>(p, qf32, kv->fmt, pl.ctas, s)
-                     : dispatch_decode<2>(p, qf32, kv->fmt, pl.ctas, s);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
-        return fail(NF_ERR_CUDA, "decode kernel set-up: %s", cudaGetErrorString(e));
-    }
-    return after_launch("decode kernel launch");
+    return run_decode(kv, q, q_dtype, batch, n_q, num_q_heads, block_table, max_blocks, seqlens, max_seqlen,
+                      softmax_scale, causal, flags, nullptr, out, out_lse, workspace, workspace_bytes, stream);
 }
 
 nf_status nf_decode_attn_noalloc(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch,
@@ -544,11 +583,29 @@ const char *nf_last_error(void) { return g_msg; }
 }  // extern "C"
 
 // ---------------------------------------------------------------- prefill
-extern "C" nf_status nf_prefill_attn(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch,
-                                     int32_t n_q, int32_t num_q_heads, const int32_t *block_table,
-                                     int32_t max_blocks, const int32_t *seqlens, int32_t max_seqlen,
-                                     float softmax_scale, int32_t causal, float *out, float *out_lse,
-                                     nf_stream_t stream) {
+namespace {
+
+// Opts a kernel in to its dynamic shared memory, once per device (a device
+// number above 63: at every call).
+template <auto Kernel>
+nf_status opt_in_smem(int bytes) {
+    static std::atomic<uint64_t> opted{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (e == cudaSuccess && (!bit || !(opted.load(std::memory_order_acquire) & bit))) {
+        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) opted.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    if (e != cudaSuccess) return fail(NF_ERR_CUDA, "prefill kernel attribute: %s", cudaGetErrorString(e));
+    return NF_OK;
+}
+
+// nf_prefill_attn and (win != nullptr) nf_prefill_attn_window.
+nf_status run_prefill(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch, int32_t n_q,
+                      int32_t num_q_heads, const int32_t *block_table, int32_t max_blocks, const int32_t *seqlens,
+                      int32_t max_seqlen, float softmax_scale, int32_t causal, const Window *win, void *out,
+                      float *out_lse, nf_stream_t stream) {
     nf_status st = check_layer(kv);
     if (st != NF_OK) return st;
     if (kv->fmt != NF_KV_K8V4) return fail(NF_ERR_UNSUPPORTED, "prefill: kv->fmt %d (only NF_KV_K8V4)", kv->fmt);
@@ -593,17 +650,17 @@ extern "C" nf_status nf_prefill_attn(const nf_kv_layer *kv, const void *q, int32
     p.max_seqlen = max_seqlen;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.causal = causal != 0;
-    p.out = out;
+    p.out = static_cast<float *>(out);
     p.out_lse = out_lse;
+    if (win) {
+        p.window = win->window;
+        p.n_sink = win->n_sink;
+        p.out_bf16 = win->out_bf16;
+    }
 
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once, [] {
-        attr_err = cudaFuncSetAttribute(nf::prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        nf::TcSmem::kBytes);
-    });
-    if (attr_err != cudaSuccess)
-        return fail(NF_ERR_CUDA, "prefill kernel attribute: %s", cudaGetErrorString(attr_err));
+    st = win ? opt_in_smem<nf::prefill_tc_kernel<true>>(nf::TcSmem::kBytes)
+             : opt_in_smem<nf::prefill_tc_kernel<false>>(nf::TcSmem::kBytes);
+    if (st != NF_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)row_tiles, (unsigned)kv->num_kv_heads, (unsigned)batch);
     cfg.blockDim = dim3(nf::kTcThreads);
@@ -614,10 +671,321 @@ extern "C" nf_status nf_prefill_attn(const nf_kv_layer *kv, const void *q, int32
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, nf::prefill_tc_kernel, p);
+    const cudaError_t e = win ? cudaLaunchKernelEx(&cfg, nf::prefill_tc_kernel<true>, p)
+                              : cudaLaunchKernelEx(&cfg, nf::prefill_tc_kernel<false>, p);
     if (e != cudaSuccess) {
         (void)cudaGetLastError();  // a refused launch leaves no sticky state for the next call
         return fail(NF_ERR_CUDA, "prefill kernel launch: %s", cudaGetErrorString(e));
     }
     return after_launch("prefill kernel launch");
 }
+
+// The planes of a pool's layers, checked: one format, one pool size.
+nf_status pool_view(const nf_kv_layer *layers, int32_t n_layers, nf::PoolView &v) {
+    if (!layers) return fail(NF_ERR_INVALID_ARG, "layers is NULL");
+    if (n_layers < 1 || n_layers > nf::kMaxLayers)
+        return fail(NF_ERR_UNSUPPORTED, "n_layers %d (1 .. %d)", n_layers, nf::kMaxLayers);
+    for (int i = 0; i < n_layers; ++i) {
+        const nf_status st = check_layer(&layers[i]);
+        if (st != NF_OK) return st;
+        if (layers[i].fmt != layers[0].fmt || layers[i].num_blocks != layers[0].num_blocks ||
+            layers[i].num_kv_heads != layers[0].num_kv_heads)
+            return fail(NF_ERR_INVALID_ARG, "layer %d differs from layer 0 in format, blocks or heads", i);
+        v.plane[i][0] = static_cast<char *>(layers[i].k_codes);
+        v.plane[i][1] = static_cast<char *>(layers[i].k_scales);
+        v.plane[i][2] = static_cast<char *>(layers[i].v_codes);
+        v.plane[i][3] = static_cast<char *>(layers[i].v_scales);
+    }
+    // bytes per (token, kv-head) of each plane
+    int per[4] = {128, 2, 128, 2};
+    switch (layers[0].fmt) {
+        case NF_KV_K8V4: per[2] = 64; per[3] = 8; break;
+        case NF_KV_K4V4: per[0] = per[2] = 64; per[1] = per[3] = 4; break;
+        case NF_KV_BF16: per[0] = per[2] = 256; per[1] = per[3] = 0; break;
+        default: break;
+    }
+    for (int k = 0; k < 4; ++k) {
+        const long long bytes = (long long)per[k] * nf::kBlock * layers[0].num_kv_heads;
+        if (bytes > (1 << 28)) return fail(NF_ERR_UNSUPPORTED, "%d kv-heads: a block above 256 MB", layers[0].num_kv_heads);
+        v.plane_bytes[k] = (int)bytes;
+    }
+    v.n_layers = n_layers;
+    v.num_blocks = layers[0].num_blocks;
+    return NF_OK;
+}
+
+// CTAs of a kernel that copies at most `pairs` blocks: enough to fill the GPU,
+// never more than there are units.
+unsigned copy_grid(const nf::PoolView &v, long long pairs, int sms) {
+    long long per_pair = 0;
+    for (int k = 0; k < 4; ++k) per_pair += (v.plane_bytes[k] + nf::kCopyPiece - 1) / nf::kCopyPiece;
+    const long long units = pairs * per_pair * v.n_layers, most = 8ll * sms;
+    return (unsigned)(units < 1 ? 1 : units < most ? units : most);
+}
+
+nf_status check_pages(const int32_t *refs, int32_t num_blocks, const int32_t *table, int32_t rows, int32_t max_blocks) {
+    if (num_blocks < 1 || num_blocks > (1 << 30))
+        return fail(NF_ERR_INVALID_ARG, "num_blocks %d (1 .. 2^30)", num_blocks);
+    if (rows < 0 || max_blocks < 1 || max_blocks > (1 << 23))
+        return fail(NF_ERR_INVALID_ARG, "rows %d / max_blocks %d", rows, max_blocks);
+    if (!refs || (rows > 0 && !table)) return fail(NF_ERR_INVALID_ARG, "a device pointer is NULL");
+    if ((reinterpret_cast<uintptr_t>(refs) | reinterpret_cast<uintptr_t>(table)) & 3)
+        return fail(NF_ERR_INVALID_ARG, "refs / block_table misaligned");
+    return NF_OK;
+}
+
+template <typename Params>
+nf_status launch(const char *what, void (*kernel)(Params), unsigned grid, unsigned block, nf_stream_t stream,
+                 const Params &p) {
+    const cudaError_t e = launch_pdl(kernel, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), p);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(NF_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    }
+    return after_launch(what);
+}
+
+nf_status done() {
+    g_msg[0] = '\0';
+    return NF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nf_status nf_prefill_attn(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch,
+                          int32_t n_q, int32_t num_q_heads, const int32_t *block_table,
+                          int32_t max_blocks, const int32_t *seqlens, int32_t max_seqlen,
+                          float softmax_scale, int32_t causal, float *out, float *out_lse,
+                          nf_stream_t stream) {
+    return run_prefill(kv, q, q_dtype, batch, n_q, num_q_heads, block_table, max_blocks, seqlens, max_seqlen,
+                       softmax_scale, causal, nullptr, out, out_lse, stream);
+}
+
+// ---------------------------------------------------------------- sliding window with sinks
+size_t nf_decode_attn_window_workspace_size(int32_t batch, int32_t n_q, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t max_seqlen, int32_t num_sms) {
+    return nf_decode_attn_workspace_size(batch, n_q, num_q_heads, num_kv_heads, max_seqlen, num_sms);
+}
+
+nf_status nf_decode_attn_window(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch, int32_t n_q,
+                                int32_t num_q_heads, const int32_t *block_table, int32_t max_blocks,
+                                const int32_t *seqlens, int32_t max_seqlen, int32_t window, int32_t n_sink,
+                                float softmax_scale, void *out, int32_t out_dtype, float *out_lse, void *workspace,
+                                size_t workspace_bytes, nf_stream_t stream) {
+    Window w;
+    const nf_status st = check_window(window, n_sink, max_seqlen, softmax_scale, out_dtype, w);
+    if (st != NF_OK) return st;
+    return run_decode(kv, q, q_dtype, batch, n_q, num_q_heads, block_table, max_blocks, seqlens, max_seqlen,
+                      softmax_scale, 1, 0u, &w, out, out_lse, workspace, workspace_bytes, stream);
+}
+
+nf_status nf_prefill_attn_window(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch, int32_t n_q,
+                                 int32_t num_q_heads, const int32_t *block_table, int32_t max_blocks,
+                                 const int32_t *seqlens, int32_t max_seqlen, int32_t window, int32_t n_sink,
+                                 float softmax_scale, void *out, int32_t out_dtype, float *out_lse,
+                                 nf_stream_t stream) {
+    Window w;
+    const nf_status st = check_window(window, n_sink, max_seqlen, softmax_scale, out_dtype, w);
+    if (st != NF_OK) return st;
+    return run_prefill(kv, q, q_dtype, batch, n_q, num_q_heads, block_table, max_blocks, seqlens, max_seqlen,
+                       softmax_scale, 1, &w, out, out_lse, stream);
+}
+
+// ---------------------------------------------------------------- rotary positions and append
+nf_status nf_rope_append_quant(const nf_kv_layer *kv, const nf_rope *rope, const int32_t *positions, const nf_heads *q,
+                               const nf_heads *k_new, const nf_heads *v_new, int32_t in_dtype, int32_t batch,
+                               int32_t n_new, int32_t num_q_heads, const int32_t *block_table, int32_t max_blocks,
+                               const int32_t *seqlens_before, const int32_t *n_valid, void *q_out,
+                               nf_stream_t stream) {
+    nf_status st = check_layer(kv);
+    if (st != NF_OK) return st;
+    if (!rope) return fail(NF_ERR_INVALID_ARG, "rope is NULL");
+    if (rope->rot_dim < 8 || rope->rot_dim > nf::kHeadDim || rope->rot_dim % 8 != 0)
+        return fail(NF_ERR_UNSUPPORTED, "rope->rot_dim %d (multiple of 8 in [8, 128])", rope->rot_dim);
+    if (rope->layout != NF_ROPE_HALVES && rope->layout != NF_ROPE_PAIRS)
+        return fail(NF_ERR_UNSUPPORTED, "rope->layout %d (NF_ROPE_HALVES or NF_ROPE_PAIRS)", rope->layout);
+    if (rope->n_axes < 1 || rope->n_axes > NF_ROPE_MAX_AXES)
+        return fail(NF_ERR_UNSUPPORTED, "rope->n_axes %d (1 .. %d)", rope->n_axes, NF_ROPE_MAX_AXES);
+    for (int i = 0; i < rope->rot_dim / 2; ++i)
+        if (rope->axis[i] >= rope->n_axes)
+            return fail(NF_ERR_INVALID_ARG, "rope->axis[%d] = %d, not below n_axes %d", i, rope->axis[i], rope->n_axes);
+    if (batch < 0 || n_new < 0 || num_q_heads < 0)
+        return fail(NF_ERR_INVALID_ARG, "batch %d / n_new %d / num_q_heads %d < 0", batch, n_new, num_q_heads);
+    if (in_dtype != NF_F32 && in_dtype != NF_BF16)
+        return fail(NF_ERR_UNSUPPORTED, "in_dtype %d (NF_F32 or NF_BF16)", in_dtype);
+    if (!q || !k_new || !v_new) return fail(NF_ERR_INVALID_ARG, "q / k_new / v_new is NULL");
+    if ((long long)batch * n_new == 0) return done();
+    if (!rope->inv_freq || !positions || !k_new->data || !v_new->data || !block_table || !seqlens_before ||
+        (num_q_heads > 0 && (!q->data || !q_out)))
+        return fail(NF_ERR_INVALID_ARG, "a device pointer is NULL");
+    if (max_blocks < 1) return fail(NF_ERR_INVALID_ARG, "max_blocks %d < 1", max_blocks);
+    const size_t align = in_dtype == NF_F32 ? 16 : 8;
+    const nf_heads *rows[3] = {q, k_new, v_new};
+    for (int i = num_q_heads > 0 ? 0 : 1; i < 3; ++i)
+        if ((reinterpret_cast<uintptr_t>(rows[i]->data) & (align - 1)) || rows[i]->batch_stride % 4 ||
+            rows[i]->token_stride % 4)
+            return fail(NF_ERR_INVALID_ARG, "q / k_new / v_new must be %zu-byte aligned, with strides in fours", align);
+    if (num_q_heads > 0 && (reinterpret_cast<uintptr_t>(q_out) & (align - 1)))
+        return fail(NF_ERR_INVALID_ARG, "q_out must be %zu-byte aligned", align);
+    const long long tokens = (long long)batch * n_new;
+    const long long total = (long long)num_q_heads + 2ll * kv->num_kv_heads;
+    const long long most = (total + nf::kRopeWarps - 1) / nf::kRopeWarps;  // one row per warp
+    if (tokens > 0x7fffffffLL || total > 0x7fffffffLL)
+        return fail(NF_ERR_INVALID_ARG, "too many tokens or heads in one append");
+    const int sms = current_sm_count();
+    if (sms < 1) return fail(NF_ERR_CUDA, "cannot query the current device");
+
+    nf::RopeParams p{};
+    p.a.k_new = k_new->data;
+    p.a.v_new = v_new->data;
+    p.a.in_f32 = in_dtype == NF_F32;
+    p.a.batch = batch;
+    p.a.n_new = n_new;
+    p.a.num_kv_heads = kv->num_kv_heads;
+    p.a.block_table = block_table;
+    p.a.max_blocks = max_blocks;
+    p.a.seqlens_before = seqlens_before;
+    p.a.num_blocks = kv->num_blocks;
+    p.a.fmt = kv->fmt;
+    p.a.k_codes = kv->k_codes;
+    p.a.k_scales = static_cast<__half *>(kv->k_scales);
+    p.a.v_codes = kv->v_codes;
+    p.a.v_scales = static_cast<__half *>(kv->v_scales);
+    p.q = q->data;
+    p.q_out = q_out;
+    p.q_bs = q->batch_stride;
+    p.q_ts = q->token_stride;
+    p.k_bs = k_new->batch_stride;
+    p.k_ts = k_new->token_stride;
+    p.v_bs = v_new->batch_stride;
+    p.v_ts = v_new->token_stride;
+    p.num_q_heads = num_q_heads;
+    p.positions = positions;
+    p.n_axes = rope->n_axes;
+    p.n_valid = n_valid;
+    p.inv_freq = rope->inv_freq;
+    p.rot = rope->rot_dim;
+    p.pairs = rope->layout == NF_ROPE_PAIRS;
+    for (int i = 0; i < rope->rot_dim / 2; ++i) p.axis[i] = rope->axis[i];
+    long long slices = (2ll * sms + tokens - 1) / tokens;
+    if (slices > most) slices = most;
+    if (slices < 1) slices = 1;  // (more than one only below 2 x SMs tokens: the grid stays below 2^31)
+    p.rows_per_slice = (int)((total + slices - 1) / slices);
+    p.slices = (int)((total + p.rows_per_slice - 1) / p.rows_per_slice);
+    return launch("rotary append kernel", nf::rope_append_kernel, (unsigned)(tokens * p.slices), nf::kRopeWarps * 32,
+                  stream, p);
+}
+
+// ---------------------------------------------------------------- pages
+nf_status nf_kv_reserve(int32_t *refs, int32_t num_blocks, int32_t *block_table, int32_t rows, int32_t max_blocks,
+                        const int32_t *from_pos, const int32_t *to_pos, nf_stream_t stream) {
+    const nf_status st = check_pages(refs, num_blocks, block_table, rows, max_blocks);
+    if (st != NF_OK) return st;
+    if (rows == 0) return done();
+    if (!from_pos || !to_pos) return fail(NF_ERR_INVALID_ARG, "a device pointer is NULL");
+    const nf::ReserveParams p{refs, num_blocks, block_table, rows, max_blocks, from_pos, to_pos};
+    return launch("page reserve kernel", nf::pages_reserve_kernel, 1, nf::kPlanThreads, stream, p);
+}
+
+nf_status nf_kv_release(int32_t *refs, int32_t num_blocks, int32_t *block_table, int32_t rows, int32_t max_blocks,
+                        const int32_t *from_pos, const int32_t *to_pos, nf_stream_t stream) {
+    const nf_status st = check_pages(refs, num_blocks, block_table, rows, max_blocks);
+    if (st != NF_OK) return st;
+    if (rows == 0) return done();
+    if (!from_pos || !to_pos) return fail(NF_ERR_INVALID_ARG, "a device pointer is NULL");
+    const nf::ReleaseParams p{refs, num_blocks, block_table, rows, max_blocks, from_pos, to_pos};
+    return launch("page release kernel", nf::pages_release_kernel, (unsigned)rows, 128, stream, p);
+}
+
+nf_status nf_kv_copy_blocks(const nf_kv_layer *layers, int32_t n_layers, const int32_t *src, const int32_t *dst,
+                            int32_t n, nf_stream_t stream) {
+    nf::CopyBlocksParams p{};
+    const nf_status st = pool_view(layers, n_layers, p.v);
+    if (st != NF_OK) return st;
+    if (n < 0) return fail(NF_ERR_INVALID_ARG, "n %d < 0", n);
+    if (n == 0) return done();
+    if (!src || !dst) return fail(NF_ERR_INVALID_ARG, "a device pointer is NULL");
+    const int sms = current_sm_count();
+    if (sms < 1) return fail(NF_ERR_CUDA, "cannot query the current device");
+    p.src = src;
+    p.dst = dst;
+    p.n = n;
+    return launch("page copy kernel", nf::copy_blocks_kernel, copy_grid(p.v, n, sms), nf::kCopyThreads, stream, p);
+}
+
+// Workspace: 16 ints of header, the moves of a compaction (two lists of at
+// most num_blocks / 2 pairs) and its new ids, or the fork's five lists.
+size_t nf_kv_pages_workspace_size(int32_t num_blocks, int32_t n_forks) {
+    if (num_blocks < 1 || num_blocks > (1 << 30) || n_forks < 0 || n_forks > nf::kMaxForks) return 0;
+    const size_t compact = 16 + 2 * ((size_t)num_blocks / 2 + 1) + (size_t)num_blocks, fork = 5 * (size_t)n_forks;
+    return ((compact > fork ? compact : fork) * 4 + 255) / 256 * 256;
+}
+
+nf_status nf_kv_fork(const nf_kv_layer *layers, int32_t n_layers, int32_t *refs, int32_t *block_table, int32_t rows,
+                     int32_t max_blocks, const int32_t *src_rows, const int32_t *dst_rows, int32_t n, int32_t *seqlens,
+                     void *workspace, size_t workspace_bytes, nf_stream_t stream) {
+    nf::ForkParams p{};
+    nf_status st = pool_view(layers, n_layers, p.v);
+    if (st != NF_OK) return st;
+    st = check_pages(refs, p.v.num_blocks, block_table, rows, max_blocks);
+    if (st != NF_OK) return st;
+    if (n < 0) return fail(NF_ERR_INVALID_ARG, "n %d < 0", n);
+    if (n > nf::kMaxForks) return fail(NF_ERR_UNSUPPORTED, "n %d pairs (at most %d in one call)", n, nf::kMaxForks);
+    if (n == 0) return done();
+    if (rows == 0 || !src_rows || !dst_rows || !seqlens)
+        return fail(NF_ERR_INVALID_ARG, "a device pointer is NULL, or the table has no rows");
+    const size_t need = 5 * (size_t)n * 4;
+    if (!workspace || workspace_bytes < need)
+        return fail(NF_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255)
+        return fail(NF_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    const int sms = current_sm_count();
+    if (sms < 1) return fail(NF_ERR_CUDA, "cannot query the current device");
+    int32_t *w = static_cast<int32_t *>(workspace);
+    p.plan = nf::ForkPlan{w, w + n, w + 2 * n, w + 3 * n, w + 4 * n};
+    p.refs = refs;
+    p.table = block_table;
+    p.rows = rows;
+    p.max_blocks = max_blocks;
+    p.src = src_rows;
+    p.dst = dst_rows;
+    p.n = n;
+    p.seqlens = seqlens;
+    st = launch("fork plan kernel", nf::fork_plan_kernel, 1, nf::kPlanThreads, stream, p);
+    if (st != NF_OK) return st;
+    return launch("fork kernel", nf::fork_apply_kernel, copy_grid(p.v, n, sms), nf::kCopyThreads, stream, p);
+}
+
+nf_status nf_kv_compact(const nf_kv_layer *layers, int32_t n_layers, int32_t *refs, int32_t *block_table, int32_t rows,
+                        int32_t max_blocks, void *workspace, size_t workspace_bytes, nf_stream_t stream) {
+    nf::CompactParams p{};
+    nf_status st = pool_view(layers, n_layers, p.v);
+    if (st != NF_OK) return st;
+    st = check_pages(refs, p.v.num_blocks, block_table, rows, max_blocks);
+    if (st != NF_OK) return st;
+    const size_t need = nf_kv_pages_workspace_size(p.v.num_blocks, 0);
+    if (!workspace || workspace_bytes < need)
+        return fail(NF_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255)
+        return fail(NF_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    const int sms = current_sm_count();
+    if (sms < 1) return fail(NF_ERR_CUDA, "cannot query the current device");
+    const int half = p.v.num_blocks / 2 + 1;
+    int32_t *w = static_cast<int32_t *>(workspace);
+    p.head = w;
+    p.src = w + 16;
+    p.dst = p.src + half;
+    p.to = p.dst + half;
+    p.refs = refs;
+    p.table = block_table;
+    p.rows = rows;
+    p.max_blocks = max_blocks;
+    st = launch("compact plan kernel", nf::compact_plan_kernel, 1, nf::kPlanThreads, stream, p);
+    if (st != NF_OK) return st;
+    return launch("compact kernel", nf::compact_apply_kernel, copy_grid(p.v, p.v.num_blocks, sms), nf::kCopyThreads,
+                  stream, p);
+}
+
+}  // extern "C"

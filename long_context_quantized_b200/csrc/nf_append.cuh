@@ -118,6 +118,56 @@ __device__ __forceinline__ void quant_row_e8(const float (&x)[4], int lane, uint
     if ((lane & 7) == 0) scales[lane >> 3] = (uint8_t)(e + 127);
 }
 
+// One K row (lane l holds channels 4l..4l+3) into slot si of the pool, in the
+// pool's format.
+__device__ __forceinline__ void store_k_row(const AppendParams &p, const float (&k)[4], int lane, size_t si) {
+    if (p.fmt == NF_KV_BF16)
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.k_codes) + si * kHeadDim + 4 * lane) =
+            make_uint2(pack_bf16(k[0], k[1]), pack_bf16(k[2], k[3]));
+    else if (p.fmt == NF_KV_K4V4)
+        quant_row_e8(k, lane, static_cast<uint8_t *>(p.k_codes) + si * (kHeadDim / 2),
+                     reinterpret_cast<uint8_t *>(p.k_scales) + si * (kHeadDim / 32));
+    else if (p.fmt == NF_KV_F8)
+        quant_row_f8(k, lane, static_cast<uint8_t *>(p.k_codes) + si * kHeadDim, p.k_scales + si);
+    else  // one int8 scale per (token, kv-head)
+        quant_row8(k, lane, static_cast<int8_t *>(p.k_codes) + si * kHeadDim, p.k_scales + si);
+}
+
+// One V row likewise.
+__device__ __forceinline__ void store_v_row(const AppendParams &p, const float (&v)[4], int lane, size_t si) {
+    if (p.fmt == NF_KV_BF16) {
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.v_codes) + si * kHeadDim + 4 * lane) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        return;
+    }
+    if (p.fmt == NF_KV_K4V4) {
+        quant_row_e8(v, lane, static_cast<uint8_t *>(p.v_codes) + si * (kHeadDim / 2),
+                     reinterpret_cast<uint8_t *>(p.v_scales) + si * (kHeadDim / 32));
+        return;
+    }
+    if (p.fmt == NF_KV_F8) {
+        quant_row_f8(v, lane, static_cast<uint8_t *>(p.v_codes) + si * kHeadDim, p.v_scales + si);
+        return;
+    }
+    if (p.fmt == NF_KV_K8V8) {
+        // int8 KV: V by the K rule
+        quant_row8(v, lane, static_cast<int8_t *>(p.v_codes) + si * kHeadDim, p.v_scales + si);
+        return;
+    }
+    // K8/V4: one scale per 32 channels = 8 lanes
+    float av = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
+    float sv;
+    const __half hv = make_scale(av, 7.0f, sv);
+    uint32_t vc = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) vc |= (uint32_t)(make_code(v[c], sv, 7) & 0xF) << (4 * c);
+    *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.v_codes) + si * (kHeadDim / 2) + 2 * lane) =
+        (uint16_t)vc;
+    if ((lane & 7) == 0) p.v_scales[si * (kHeadDim / kVGroup) + (lane >> 3)] = hv;
+}
+
 __global__ void __launch_bounds__(256) append_quant_kernel(const AppendParams p) {
     // let the next kernel place its CTAs at once (it waits for this grid to
     // complete before it reads what this one writes)
@@ -152,49 +202,8 @@ __global__ void __launch_bounds__(256) append_quant_kernel(const AppendParams p)
     }
     const size_t si = ((size_t)blk * p.num_kv_heads + h) * kBlock + (pos & (kBlock - 1));
 
-    if (p.fmt == NF_KV_BF16) {
-        uint2 kb, vb;
-        kb.x = pack_bf16(k[0], k[1]); kb.y = pack_bf16(k[2], k[3]);
-        vb.x = pack_bf16(v[0], v[1]); vb.y = pack_bf16(v[2], v[3]);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.k_codes) + si * kHeadDim + 4 * lane) = kb;
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.v_codes) + si * kHeadDim + 4 * lane) = vb;
-        return;
-    }
-
-    if (p.fmt == NF_KV_K4V4) {
-        quant_row_e8(k, lane, static_cast<uint8_t *>(p.k_codes) + si * (kHeadDim / 2),
-                     reinterpret_cast<uint8_t *>(p.k_scales) + si * (kHeadDim / 32));
-        quant_row_e8(v, lane, static_cast<uint8_t *>(p.v_codes) + si * (kHeadDim / 2),
-                     reinterpret_cast<uint8_t *>(p.v_scales) + si * (kHeadDim / 32));
-        return;
-    }
-
-    if (p.fmt == NF_KV_F8) {
-        quant_row_f8(k, lane, static_cast<uint8_t *>(p.k_codes) + si * kHeadDim, p.k_scales + si);
-        quant_row_f8(v, lane, static_cast<uint8_t *>(p.v_codes) + si * kHeadDim, p.v_scales + si);
-        return;
-    }
-
-    // ---- K: one scale per (token, kv-head)
-    quant_row8(k, lane, static_cast<int8_t *>(p.k_codes) + si * kHeadDim, p.k_scales + si);
-    if (p.fmt == NF_KV_K8V8) {
-        // int8 KV: V by the same rule
-        quant_row8(v, lane, static_cast<int8_t *>(p.v_codes) + si * kHeadDim, p.v_scales + si);
-        return;
-    }
-
-    // ---- V: one scale per 32 channels = 8 lanes
-    float av = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
-    float sv;
-    const __half hv = make_scale(av, 7.0f, sv);
-    uint32_t vc = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) vc |= (uint32_t)(make_code(v[c], sv, 7) & 0xF) << (4 * c);
-    *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.v_codes) + si * (kHeadDim / 2) + 2 * lane) =
-        (uint16_t)vc;
-    if ((lane & 7) == 0) p.v_scales[si * (kHeadDim / kVGroup) + (lane >> 3)] = hv;
+    store_k_row(p, k, lane, si);
+    store_v_row(p, v, lane, si);
 }
 
 }  // namespace nf

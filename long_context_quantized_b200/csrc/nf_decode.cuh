@@ -175,7 +175,47 @@ struct DecodeParams {
     int32_t *claims;   // [gridDim.x + batch * H_kv] share flags, indexed like the slots; zero between calls
     float *partials;   // [gridDim.x + batch * H_kv] slots of slot_floats
     int slot_floats;   // rows * 128 (o) + rows (lse), rounded up to 4 floats
+    // windowed calls only: a query at position P sees keys t <= P with t > P - window or t < n_sink
+    int window, n_sink;
+    int out_bf16;  // out holds bf16 (o rounded once) instead of fp32
 };
+
+// The part of a sequence of L keys that a windowed call reads, in chunks of
+// kChunk keys: [0, sinks) and [sinks + skip, end).  Every key between the two
+// is hidden from all n_q queries; where the two would touch or overlap,
+// everything from chunk 0 is read (sinks = skip = 0).  lo is the first window
+// position of query 0, the lowest of any query: a key t with n_sink <= t < lo
+// is seen by no query.
+struct WinSpan {
+    int sinks, skip, lo;
+};
+__host__ __device__ __forceinline__ WinSpan win_span(int L, int n_q, int window, int n_sink) {
+    WinSpan w{0, 0, L - n_q - window + 1};
+    if (w.lo < 0) w.lo = 0;
+    if (n_sink < w.lo) {
+        const int s = (n_sink + kChunk - 1) / kChunk, first = w.lo / kChunk;
+        if (s < first) {
+            w.sinks = s;
+            w.skip = first - s;
+        }
+    }
+    return w;
+}
+// What decode_unit needs of the window: masks of rows (window, n_sink) and of
+// keys no row sees (lo).
+struct WinMask {
+    int window, n_sink, lo;
+};
+
+// Four output channels of a row: fp32, or (windowed calls that ask for it) bf16.
+template <bool WIN>
+__device__ __forceinline__ void store_out4(float *out, int bf16, size_t row, int c4, const float4 &o) {
+    if (WIN && bf16)
+        reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(out) + row * kHeadDim)[c4] =
+            make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    else
+        reinterpret_cast<float4 *>(out + row * kHeadDim)[c4] = o;
+}
 
 template <int NT, int FMT>
 struct DecodeSmem {
@@ -300,9 +340,13 @@ struct LaneOffsets {
 // One work unit of a consumer warp: MT m-tiles of 16 keys starting at key ub
 // of the stage buffer st (key tok0 + ub of the segment).  FAST: every row sees
 // every key of the unit, so no mask is applied.
-template <int NT, int MT, bool QF32, int FMT, bool FAST>
+// WIN: the windowed masks too.
+template <int NT, int MT, bool QF32, int FMT, bool FAST, bool WIN>
 __device__ __forceinline__ void decode_unit(WarpState<NT, QF32, FMT> &ws, const unsigned char *st, int ub,
-                                            int tok0, int L, int lane, const LaneOffsets &lo) {
+                                            int tok0, int L, int lane, const LaneOffsets &lo, const WinMask &wm) {
+    // a key that some row may see; the bytes of the others (stale, released or
+    // not a number) must not reach the products
+    auto alive = [&](int pos) { return pos < L && (!WIN || pos >= wm.lo || pos < wm.n_sink); };
     using ST = Stage<FMT, NT>;
     constexpr bool K8 = FMT == NF_KV_K8V4 || FMT == NF_KV_K8V8;  // int8 K codes
     constexpr bool K4 = FMT == NF_KV_K4V4;                         // 4-bit K and V, exponent-byte scales
@@ -420,12 +464,14 @@ __device__ __forceinline__ void decode_unit(WarpState<NT, QF32, FMT> &ws, const 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int pos = tok0 + tb + 8 * (i >> 1) + 2 * t + (i & 1);
-                    if (!(pos < L && pos <= ws.lim[nt])) xv[mt][nt][i] = -INFINITY;
+                    bool see = pos < L && pos <= ws.lim[nt];
+                    if (WIN) see = see && (pos > ws.lim[nt] - wm.window || pos < wm.n_sink);
+                    if (!see) xv[mt][nt][i] = -INFINITY;
                 }
             if (K4) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (!(tok0 + tb + 8 * (i >> 1) + 2 * t + (i & 1) < L)) rl[mt][i] = 0.f;
+                    if (!alive(tok0 + tb + 8 * (i >> 1) + 2 * t + (i & 1))) rl[mt][i] = 0.f;
             }
         }
     }
@@ -509,8 +555,8 @@ __device__ __forceinline__ void decode_unit(WarpState<NT, QF32, FMT> &ws, const 
             uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
             if (!FAST) {
                 const int pa = tok0 + tb + 2 * t;
-                keep0 = (pa < L ? 0x0000FFFFu : 0u) | (pa + 1 < L ? 0xFFFF0000u : 0u);
-                keep1 = (pa + 8 < L ? 0x0000FFFFu : 0u) | (pa + 9 < L ? 0xFFFF0000u : 0u);
+                keep0 = (alive(pa) ? 0x0000FFFFu : 0u) | (alive(pa + 1) ? 0xFFFF0000u : 0u);
+                keep1 = (alive(pa + 8) ? 0x0000FFFFu : 0u) | (alive(pa + 9) ? 0xFFFF0000u : 0u);
                 sp0 &= keep0;
                 sp1 &= keep1;
             }
@@ -586,7 +632,7 @@ __device__ __forceinline__ void decode_unit(WarpState<NT, QF32, FMT> &ws, const 
                 if (!FAST) {
                     // keys past the end hold stale bytes: zero their scales
                     const int pa = tok0 + tb + 8 * kh + 2 * t;
-                    const uint32_t keep = (pa < L ? 0x0000FFFFu : 0u) | (pa + 1 < L ? 0xFFFF0000u : 0u);
+                    const uint32_t keep = (alive(pa) ? 0x0000FFFFu : 0u) | (alive(pa + 1) ? 0xFFFF0000u : 0u);
 #pragma unroll
                     for (int cg = 0; cg < 4; ++cg) sp[kh][cg] &= keep;
                 }
@@ -610,7 +656,7 @@ __device__ __forceinline__ void decode_unit(WarpState<NT, QF32, FMT> &ws, const 
             }
         } else {
             const unsigned char *v0p = st + ST::kV + tb * 256 + lo.v;
-            const bool ok0 = FAST || tok0 + tb + g < L, ok1 = FAST || tok0 + tb + g + 8 < L;
+            const bool ok0 = FAST || alive(tok0 + tb + g), ok1 = FAST || alive(tok0 + tb + g + 8);
             uint32_t w0[16], w1[16];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -766,6 +812,7 @@ struct OutRows {
     float *out, *out_lse;
     size_t base;  // row index of (b, query 0, first q-head of the group)
     int group, n_q, num_q_heads;
+    int bf16;  // windowed calls only: out holds bf16
     __device__ size_t operator()(int r) const {
         return base + (size_t)(r / group) * num_q_heads + r % group;
     }
@@ -805,7 +852,7 @@ __device__ __noinline__ void merge_weights(const float *src, size_t sf, int n, i
     }
 }
 
-template <int NTHR, bool SMEM>
+template <int NTHR, bool SMEM, bool WIN>
 __device__ __noinline__ void merge_items(const float *src, size_t sf, int n, int r0, int nr, const float *wsm,
                                          const OutRows orow) {
     constexpr int KB = 16;
@@ -832,7 +879,7 @@ __device__ __noinline__ void merge_items(const float *src, size_t sf, int n, int
                 acc.w = fmaf(wk, o[j].w, acc.w);
             }
         }
-        reinterpret_cast<float4 *>(orow.out + orow(r) * kHeadDim)[c4] = acc;
+        store_out4<WIN>(orow.out, orow.bf16, orow(r), c4, acc);
     }
 }
 
@@ -847,7 +894,7 @@ __device__ __noinline__ void merge_items(const float *src, size_t sf, int n, int
 // (wcap floats), one bulk copy brings the slots into the ring while the
 // weights are worked out from L2, and the items read shared memory; else the
 // merge reads L2, in passes of as many rows as wsm holds.
-template <int NTHR, uint32_t BAR>
+template <int NTHR, uint32_t BAR, bool WIN>
 __device__ __forceinline__ void finish_piece_single(const DecodeParams &p, int s_id, int first, int n, int rows,
                                                     int b, int h, bool ring_idle, unsigned char *ring,
                                                     uint32_t ring_bytes, uint64_t *fin_bar, uint32_t &fin_phase,
@@ -872,7 +919,7 @@ __device__ __forceinline__ void finish_piece_single(const DecodeParams &p, int s
     named_sync(BAR, NTHR);
     if (!misc[1]) return;
     const OutRows orow{p.out, p.out_lse, (size_t)b * p.n_q * p.num_q_heads + (size_t)h * p.group, p.group, p.n_q,
-                       p.num_q_heads};
+                       p.num_q_heads, WIN ? p.out_bf16 : 0};
     if (in_ring) {
         merge_weights<NTHR>(slots, sf, n, rows, 0, rows, wsm, orow);  // while the copy is in flight
         if (!misc[0] && !mbar_wait(fin_bar, fin_phase)) {
@@ -882,16 +929,16 @@ __device__ __forceinline__ void finish_piece_single(const DecodeParams &p, int s
         fin_phase ^= 1u;
         named_sync(BAR, NTHR);
         if (!misc[0])
-            merge_items<NTHR, true>(reinterpret_cast<const float *>(ring), sf, n, 0, rows, wsm, orow);
+            merge_items<NTHR, true, WIN>(reinterpret_cast<const float *>(ring), sf, n, 0, rows, wsm, orow);
         else  // after a timeout the slots are read from L2 instead
-            merge_items<NTHR, false>(slots, sf, n, 0, rows, wsm, orow);
+            merge_items<NTHR, false, WIN>(slots, sf, n, 0, rows, wsm, orow);
     } else {
         const int rpp = min(rows, max(1, wcap / n));
         for (int r0 = 0; r0 < rows; r0 += rpp) {
             const int nr = min(rpp, rows - r0);
             merge_weights<NTHR>(slots, sf, n, rows, r0, nr, wsm, orow);
             named_sync(BAR, NTHR);
-            merge_items<NTHR, false>(slots, sf, n, r0, nr, wsm, orow);
+            merge_items<NTHR, false, WIN>(slots, sf, n, r0, nr, wsm, orow);
             named_sync(BAR, NTHR);  // wsm is free again
         }
     }
@@ -953,7 +1000,11 @@ __device__ __forceinline__ void finish_piece_coop(const DecodeParams &p, int s_i
     }
 }
 
-template <int NT, bool QF32, int FMT>
+// WIN: the windowed form (nf_decode_attn_window).  A sequence's chunk list is
+// its sinks' chunks and its window's (win_span); positions of the work cut
+// count in that list, and each stage maps them to keys.  A sequence of length
+// 0 is an unused row of the batch.
+template <int NT, bool QF32, int FMT, bool WIN>
 __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
     using ST = Stage<FMT, NT>;
     using SM = DecodeSmem<NT, FMT>;
@@ -1013,8 +1064,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         for (int b = lane; b < p.batch; b += 32) {
             const int L = p.seqlens[b];
             const bool ok = L >= p.n_q && L <= p.max_seqlen;
-            if (!ok && blockIdx.x == 0) report(NF_DEVERR_SEQLEN);
-            seqC[b] = ok ? (L + kChunk - 1) / kChunk : 0;
+            if (!ok && blockIdx.x == 0 && !(WIN && L == 0)) report(NF_DEVERR_SEQLEN);
+            seqC[b] = ok ? (L + kChunk - 1) / kChunk - (WIN ? win_span(L, p.n_q, p.window, p.n_sink).skip : 0) : 0;
             seqL[b] = ok ? L : 0;
         }
         __syncwarp();
@@ -1051,13 +1102,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         bool waited = !p.early_kv;
         while (!stop && walk.next()) {
             const int32_t *bt = p.block_table + (size_t)walk.pb * p.max_blocks;
-            const int nblk = (seqC[walk.pb] * kChunk + kBlock - 1) / kBlock;
+            const WinSpan span = WIN ? win_span(seqL[walk.pb], p.n_q, p.window, p.n_sink) : WinSpan{0, 0, 0};
+            const int nblk = ((seqC[walk.pb] + (WIN ? span.skip : 0)) * kChunk + kBlock - 1) / kBlock;
             int win = -1000000, my_blk = 0;
             const int cx1 = (int)(walk.xe - walk.s0);
             for (int cx = (int)(walk.xs - walk.s0); cx < cx1; ++kst) {
-                const int ce = stage_end<FMT, NT>(cx, cx1);
-                const int tok0 = cx * kChunk, ntok = (ce - cx) * kChunk;
-                cx = ce;
+                const int off = WIN && cx >= span.sinks ? span.skip : 0;  // list position -> chunk
+                const int ce = stage_end<FMT, NT>(cx + off, (WIN && cx < span.sinks ? min(cx1, span.sinks) : cx1) + off);
+                const int tok0 = (cx + off) * kChunk, ntok = (ce - cx - off) * kChunk;
+                cx = ce - off;
                 if (!waited && tok0 + ntok > seqL[walk.pb] - p.n_q) {
                     pdl_wait();  // the newest rows may come from the kernels before this one
                     waited = true;
@@ -1151,7 +1204,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
             const int r = idx / kHeadDim, ch = idx % kHeadDim;
             const int j = r / p.group, gq = r % p.group;
             const size_t row = ((size_t)b * p.n_q + j) * p.num_q_heads + (size_t)h * p.group + gq;
-            p.out[row * kHeadDim + ch] = 0.f;
+            if (WIN && p.out_bf16)
+                reinterpret_cast<__nv_bfloat16 *>(p.out)[row * kHeadDim + ch] = __float2bfloat16_rn(0.f);
+            else
+                p.out[row * kHeadDim + ch] = 0.f;
             if (ch == 0 && p.out_lse) p.out_lse[row] = -INFINITY;
         }
     }
@@ -1333,12 +1389,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         }
         // keys every row of the group sees, for the no-mask fast path
         const int all_see = p.causal ? L - p.n_q + 1 : L;
+        const WinSpan span = WIN ? win_span(L, p.n_q, p.window, p.n_sink) : WinSpan{0, 0, 0};
+        const WinMask wm{p.window, p.n_sink, span.lo};
 
         const int cx1 = (int)(walk.xe - walk.s0);
         for (int cx = (int)(walk.xs - walk.s0); cx < cx1;) {
-            const int ce = stage_end<FMT, NT>(cx, cx1);
-            const int tok0 = cx * kChunk, n_units = (ce - cx) * (kChunk / (16 * MT));
-            cx = ce;
+            const int off = WIN && cx >= span.sinks ? span.skip : 0;
+            const int ce = stage_end<FMT, NT>(cx + off, (WIN && cx < span.sinks ? min(cx1, span.sinks) : cx1) + off);
+            const int tok0 = (cx + off) * kChunk, n_units = (ce - cx - off) * (kChunk / (16 * MT));
+            cx = ce - off;
             if (!misc[0] && !mbar_wait(&full[stage], phase)) {
                 report(NF_DEVERR_TIMEOUT);
                 misc[0] = 1;
@@ -1347,10 +1406,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
                 const unsigned char *st = smem + stage * ST::kStride;
                 for (int un = slot; un < n_units; un += CW) {
                     const int ub = 16 * MT * un;  // first key of the unit in the stage
-                    if (tok0 + ub + 16 * MT <= all_see)
-                        decode_unit<NT, MT, QF32, FMT, true>(ws, st, ub, tok0, L, lane, lo);
+                    // windowed: the keys are sinks, or inside the last query's window
+                    const bool fast = tok0 + ub + 16 * MT <= all_see &&
+                                      (!WIN || tok0 + ub + 16 * MT <= p.n_sink || tok0 + ub >= L - p.window);
+                    if (fast)
+                        decode_unit<NT, MT, QF32, FMT, true, WIN>(ws, st, ub, tok0, L, lane, lo, wm);
                     else
-                        decode_unit<NT, MT, QF32, FMT, false>(ws, st, ub, tok0, L, lane, lo);
+                        decode_unit<NT, MT, QF32, FMT, false, WIN>(ws, st, ub, tok0, L, lane, lo, wm);
                 }
             }
             __syncwarp();
@@ -1423,7 +1485,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
                 if (n_pieces == 1) {
                     const int j = r / p.group, gq = r % p.group;
                     const size_t row = ((size_t)b * p.n_q + j) * p.num_q_heads + (size_t)h * p.group + gq;
-                    reinterpret_cast<float4 *>(p.out + row * kHeadDim)[c4] = o;
+                    store_out4<WIN>(p.out, p.out_bf16, row, c4, o);
                     if (c4 == 0 && p.out_lse) p.out_lse[row] = lse;
                 } else {
                     reinterpret_cast<float4 *>(slotp + r * kHeadDim)[c4] = o;
@@ -1434,7 +1496,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         named_sync(1, kConsumerWarps * 32);
         PieceWalker rest = walk;
         const bool more = rest.next();  // another piece follows: its stages may be in the ring
-        finish_piece_single<kConsumerWarps * 32, 1>(p, s_id, first, n_pieces, rows_here, b, h, !more, smem,
+        finish_piece_single<kConsumerWarps * 32, 1, WIN>(p, s_id, first, n_pieces, rows_here, b, h, !more, smem,
                                                     NS * ST::kStride, fin_bar, fin_phase, sm_o, SM::kMergeFloats,
                                                     misc);
     }
