@@ -78,6 +78,8 @@ def library_path() -> str:
 def load_library():
     """Load libnf.so (built by ``python -m long_context_quantized_b200.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -154,8 +156,8 @@ def _dptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -190,6 +192,7 @@ class KVLayer:
                              k_codes.data_ptr(), 0 if k_scales is None else k_scales.data_ptr(),
                              v_codes.data_ptr(), 0 if v_scales is None else v_scales.data_ptr())
         self.ref = ctypes.byref(self.c)
+        self.device = k_codes.get_device()
 
     @classmethod
     def empty(cls, fmt: int, num_blocks: int, num_kv_heads: int, device="cuda", fill: int | None = None):
@@ -379,21 +382,23 @@ def _refuse(where, message):
     raise NfError(NF_ERR_INVALID_ARG, where, message)
 
 
-def _same_device(where, device, **tensors):
-    """Every tensor contiguous, of its dtype, on `device`, which is the current one."""
-    if device.type != "cuda":
+# The checks below run at every call, a few hundred nanoseconds each: a call's
+# host time is most of what a short kernel costs its caller.
+def _current(where, t) -> int:
+    """The device number of t, which must be the current CUDA device."""
+    d = t.get_device()
+    if d < 0:
         _refuse(where, "tensors must be on a CUDA device")
-    if device.index != torch.cuda.current_device():
-        _refuse(where, f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, (t, dtype) in tensors.items():
-        if t is None:
-            continue
-        if t.device != device:
-            _refuse(where, f"{name} is on {t.device}, expected {device}")
-        if not t.is_contiguous():
-            _refuse(where, f"{name} must be contiguous")
-        if t.dtype != dtype:
-            _refuse(where, f"{name}: dtype {t.dtype}, expected {dtype}")
+    if d != torch.cuda.current_device():
+        _refuse(where, f"tensors are on cuda:{d}, the current device is cuda:{torch.cuda.current_device()}")
+    return d
+
+
+def _on(where, name, t, device: int, dtype):
+    """t must be contiguous, of dtype, on the device."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(where, f"{name}: {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}; "
+                       f"expected a contiguous {dtype} tensor on cuda:{device}")
 
 
 def nf_decode_attn_window_workspace_size(batch, n_q, num_q_heads, num_kv_heads, max_seqlen, num_sms=None):
@@ -404,18 +409,25 @@ def nf_decode_attn_window_workspace_size(batch, n_q, num_q_heads, num_kv_heads, 
 
 
 def _window_args(where, kv, q, block_table, seqlens, out, out_lse):
-    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
-        _refuse(where, "q must be [batch][n_q][H_q][128]")
-    _same_device(where, q.device, q=(q, q.dtype), block_table=(block_table, torch.int32),
-                 seqlens=(seqlens, torch.int32), out=(out, out.dtype), out_lse=(out_lse, torch.float32))
-    if kv.k_codes.device != q.device:
-        _refuse(where, f"the pool is on {kv.k_codes.device}, q on {q.device}")
-    if out.shape != q.shape:
+    """Checks what both windowed calls take; returns q's shape and device."""
+    d = _current(where, q)
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != HEAD_DIM or not q.is_contiguous():
+        _refuse(where, "q must be contiguous [batch][n_q][H_q][128]")
+    _on(where, "block_table", block_table, d, torch.int32)
+    _on(where, "seqlens", seqlens, d, torch.int32)
+    _on(where, "out", out, d, out.dtype)
+    if kv.device != d:
+        _refuse(where, f"the pool is on cuda:{kv.device}, q on cuda:{d}")
+    if out.shape != shape:
         _refuse(where, "out must have q's shape")
-    if out_lse is not None and out_lse.shape != q.shape[:3]:
-        _refuse(where, "out_lse must be [batch][n_q][H_q]")
-    if block_table.dim() != 2 or block_table.shape[0] != q.shape[0] or seqlens.shape != q.shape[:1]:
+    if out_lse is not None:
+        _on(where, "out_lse", out_lse, d, torch.float32)
+        if out_lse.shape != shape[:3]:
+            _refuse(where, "out_lse must be [batch][n_q][H_q]")
+    if block_table.dim() != 2 or len(block_table) != shape[0] or seqlens.dim() != 1 or len(seqlens) != shape[0]:
         _refuse(where, "block_table [batch][max_blocks] and seqlens [batch] must have q's batch")
+    return shape, d
 
 
 def nf_decode_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int, window: int, n_sink: int,
@@ -424,12 +436,11 @@ def nf_decode_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int,
     sees the keys t <= P with t > P - window or t < n_sink (see nf.h).  out
     (fp32 or bf16) has the shape of q [batch][n_q][H_q][128]; seqlens 0 marks an
     unused row of the batch."""
-    _window_args("nf_decode_attn_window", kv, q, block_table, seqlens, out, out_lse)
+    (B, n_q, H_q, _), d = _window_args("nf_decode_attn_window", kv, q, block_table, seqlens, out, out_lse)
     if workspace is None:
         raise NfError(NF_ERR_WORKSPACE, "nf_decode_attn_window", "workspace tensor required "
                       "(size: nf_decode_attn_window_workspace_size)")
-    _same_device("nf_decode_attn_window", q.device, workspace=(workspace, workspace.dtype))
-    B, n_q, H_q, _ = q.shape
+    _on("nf_decode_attn_window", "workspace", workspace, d, workspace.dtype)
     st = load_library().nf_decode_attn_window(
         kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1],
         seqlens.data_ptr(), max_seqlen, window, n_sink, softmax_scale, out.data_ptr(), _dtype_code(out.dtype),
@@ -441,8 +452,7 @@ def nf_prefill_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int
                            softmax_scale: float, out, out_lse=None, stream=None):
     """Chunked-prefill attention with a sliding window and sinks (see nf.h and
     nf_decode_attn_window): bf16 q over a K8/V4 pool, out fp32 or bf16."""
-    _window_args("nf_prefill_attn_window", kv, q, block_table, seqlens, out, out_lse)
-    B, n_q, H_q, _ = q.shape
+    (B, n_q, H_q, _), d = _window_args("nf_prefill_attn_window", kv, q, block_table, seqlens, out, out_lse)
     st = load_library().nf_prefill_attn_window(
         kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1],
         seqlens.data_ptr(), max_seqlen, window, n_sink, softmax_scale, out.data_ptr(), _dtype_code(out.dtype),
@@ -462,18 +472,17 @@ class Rope:
         axis = [0] * half if axis is None else [int(a) for a in axis]
         if len(axis) != half or half > 64 or any(not 0 <= a < n_axes for a in axis):
             _refuse("Rope", "axis must hold one axis below n_axes for each of the (at most 64) frequencies")
-        self.inv_freq, self.n_axes = inv_freq, int(n_axes)
+        self.inv_freq, self.n_axes, self.device = inv_freq, int(n_axes), inv_freq.get_device()
         self.c = nf_rope(2 * half, layout, n_axes, (ctypes.c_uint8 * 64)(*axis), inv_freq.data_ptr())
         self.ref = ctypes.byref(self.c)
 
 
-def _heads(where, name, t, dtype, device, batch, n_new):
-    if t.dim() != 4 or t.shape[0] != batch or t.shape[1] != n_new or t.shape[3] != HEAD_DIM:
-        _refuse(where, f"{name} must be [batch][n_new][heads][128]")
-    if t.dtype != dtype or t.device != device:
-        _refuse(where, f"{name}: {t.dtype} on {t.device}, expected {dtype} on {device}")
+def _heads(where, name, t, dtype, device, batch, n_new, heads):
+    if t.shape != (batch, n_new, heads, HEAD_DIM) or t.dtype is not dtype or t.get_device() != device:
+        _refuse(where, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} "
+                       f"{(batch, n_new, heads, HEAD_DIM)} on cuda:{device}")
     sb, st, sh, sc = t.stride()
-    if (sc != 1 or (sh != HEAD_DIM and t.shape[2] > 1)) and t.numel():
+    if (sc != 1 or (sh != HEAD_DIM and heads > 1)) and t.numel():
         _refuse(where, f"{name}: the heads of a token must be contiguous")
     return nf_heads(t.data_ptr(), sb, st)
 
@@ -487,32 +496,41 @@ def nf_rope_append_quant(kv: KVLayer, rope: Rope, positions, q, k_new, v_new, bl
     strided views (of a fused projection's output) whose heads are contiguous;
     tokens from n_valid[b] on are padding.  q and q_out may be None."""
     where = "nf_rope_append_quant"
+    d = _current(where, k_new)
+    if k_new.dim() != 4:
+        _refuse(where, "k_new must be [batch][n_new][H_kv][128]")
     B, n_new = k_new.shape[0], k_new.shape[1]
-    dtype, device = k_new.dtype, k_new.device
-    k = _heads(where, "k_new", k_new, dtype, device, B, n_new)
-    v = _heads(where, "v_new", v_new, dtype, device, B, n_new)
-    if k_new.shape[2] != kv.num_kv_heads or v_new.shape[2] != kv.num_kv_heads:
-        _refuse(where, f"k_new / v_new must have the pool's {kv.num_kv_heads} heads")
-    H_q = 0
-    qh = nf_heads(None, 0, 0)
+    dtype = k_new.dtype
+    k = _heads(where, "k_new", k_new, dtype, d, B, n_new, kv.num_kv_heads)
+    v = _heads(where, "v_new", v_new, dtype, d, B, n_new, kv.num_kv_heads)
     if q is not None:
-        qh = _heads(where, "q", q, dtype, device, B, n_new)
-        H_q = q.shape[2]
+        H_q = q.shape[2] if q.dim() == 4 else 0
+        qh = _heads(where, "q", q, dtype, d, B, n_new, H_q)
         if q_out is None or q_out.shape != q.shape:
             _refuse(where, "q_out must have q's shape")
-    _same_device(where, device, positions=(positions, torch.int32), block_table=(block_table, torch.int32),
-                 seqlens_before=(seqlens_before, torch.int32), n_valid=(n_valid, torch.int32), q_out=(q_out, dtype))
-    if kv.k_codes.device != device or rope.inv_freq.device != device:
+        _on(where, "q_out", q_out, d, dtype)
+        out = q_out.data_ptr()
+    else:
+        H_q, qh, out = 0, nf_heads(None, 0, 0), None
+    _on(where, "positions", positions, d, torch.int32)
+    _on(where, "block_table", block_table, d, torch.int32)
+    _on(where, "seqlens_before", seqlens_before, d, torch.int32)
+    if kv.device != d or rope.device != d:
         _refuse(where, "the pool, inv_freq and the inputs must be on one device")
     if positions.shape != (B, n_new, rope.n_axes):
         _refuse(where, f"positions must be [batch][n_new][{rope.n_axes}]")
-    if (block_table.dim() != 2 or block_table.shape[0] != B or seqlens_before.shape != (B,)
-            or (n_valid is not None and n_valid.shape != (B,))):
-        _refuse(where, "block_table, seqlens_before and n_valid must have the inputs' batch")
+    if block_table.dim() != 2 or len(block_table) != B or seqlens_before.shape != (B,):
+        _refuse(where, "block_table and seqlens_before must have the inputs' batch")
+    valid = None
+    if n_valid is not None:
+        _on(where, "n_valid", n_valid, d, torch.int32)
+        if n_valid.shape != (B,):
+            _refuse(where, "n_valid must be [batch]")
+        valid = n_valid.data_ptr()
     st = load_library().nf_rope_append_quant(
         kv.ref, rope.ref, positions.data_ptr(), ctypes.byref(qh), ctypes.byref(k), ctypes.byref(v), _dtype_code(dtype),
-        B, n_new, H_q, block_table.data_ptr(), block_table.shape[1], seqlens_before.data_ptr(),
-        None if n_valid is None else n_valid.data_ptr(), None if q_out is None else q_out.data_ptr(), _stream(stream))
+        B, n_new, H_q, block_table.data_ptr(), block_table.shape[1], seqlens_before.data_ptr(), valid, out,
+        _stream(stream))
     _check(st, where)
 
 
@@ -524,9 +542,8 @@ class KVLayers:
         self.layers = list(layers)
         if not self.layers:
             _refuse("KVLayers", "no layers")
-        self.num_blocks = self.layers[0].num_blocks
-        self.device = self.layers[0].k_codes.device
-        if any(layer.k_codes.device != self.device for layer in self.layers):
+        self.num_blocks, self.device = self.layers[0].num_blocks, self.layers[0].device
+        if any(layer.device != self.device for layer in self.layers):
             _refuse("KVLayers", "the layers must be on one device")
         self.c = (nf_kv_layer * len(self.layers))(*[layer.c for layer in self.layers])
 
@@ -534,43 +551,58 @@ class KVLayers:
         return len(self.layers)
 
 
-def _pages_args(where, refs, block_table, rows_of=(), **more):
-    _same_device(where, refs.device, refs=(refs, torch.int32), block_table=(block_table, torch.int32), **more)
+def _pages_args(where, refs, block_table) -> int:
+    d = _current(where, refs)
+    _on(where, "refs", refs, d, torch.int32)
+    _on(where, "block_table", block_table, d, torch.int32)
     if refs.dim() != 1 or block_table.dim() != 2:
         _refuse(where, "refs must be [num_blocks], block_table [rows][max_blocks]")
-    for name in rows_of:
-        if more[name][0].shape != block_table.shape[:1]:
-            _refuse(where, f"{name} must be [rows]")
+    return d
 
 
-def _range_call(where, refs, block_table, from_pos, to_pos, stream):
-    _pages_args(where, refs, block_table, ("from_pos", "to_pos"), from_pos=(from_pos, torch.int32),
-                to_pos=(to_pos, torch.int32))
-    st = getattr(load_library(), where)(refs.data_ptr(), refs.shape[0], block_table.data_ptr(), block_table.shape[0],
-                                        block_table.shape[1], from_pos.data_ptr(), to_pos.data_ptr(), _stream(stream))
-    _check(st, where)
+def _pool_args(where, layers, refs, block_table, workspace) -> int:
+    d = _pages_args(where, refs, block_table)
+    if len(refs) != layers.num_blocks or layers.device != d:
+        _refuse(where, "refs must have one count per block of the pool, on its device")
+    _on(where, "workspace", workspace, d, workspace.dtype)
+    return d
+
+
+def _rows(where, name, t, d, n):
+    _on(where, name, t, d, torch.int32)
+    if t.dim() != 1 or len(t) != n:
+        _refuse(where, f"{name}: {tuple(t.shape)}, expected [{n}]")
+    return t.data_ptr()
+
+
+def _range_call(where, call, refs, block_table, from_pos, to_pos, stream):
+    d = _pages_args(where, refs, block_table)
+    rows, width = block_table.shape
+    _check(call(refs.data_ptr(), len(refs), block_table.data_ptr(), rows, width, _rows(where, "from_pos", from_pos, d, rows),
+                _rows(where, "to_pos", to_pos, d, rows), _stream(stream)), where)
 
 
 def nf_kv_reserve(refs, block_table, from_pos, to_pos, stream=None):
     """Fresh pages for the positions [from_pos[b], to_pos[b]) of every table
     row that have none (see nf.h): the lowest free blocks, in row order."""
-    _range_call("nf_kv_reserve", refs, block_table, from_pos, to_pos, stream)
+    _range_call("nf_kv_reserve", load_library().nf_kv_reserve, refs, block_table, from_pos, to_pos, stream)
 
 
 def nf_kv_release(refs, block_table, from_pos, to_pos, stream=None):
     """Give up the pages wholly inside [from_pos[b], to_pos[b]) of every table
     row (see nf.h): behind a window, or a whole sequence."""
-    _range_call("nf_kv_release", refs, block_table, from_pos, to_pos, stream)
+    _range_call("nf_kv_release", load_library().nf_kv_release, refs, block_table, from_pos, to_pos, stream)
 
 
 def nf_kv_copy_blocks(layers: KVLayers, src, dst, stream=None):
     """Copy block src[i] to dst[i] in every layer (int32 [n]; see nf.h)."""
     where = "nf_kv_copy_blocks"
-    _same_device(where, layers.device, src=(src, torch.int32), dst=(dst, torch.int32))
-    if src.dim() != 1 or src.shape != dst.shape:
-        _refuse(where, "src and dst must be [n]")
-    st = load_library().nf_kv_copy_blocks(layers.c, len(layers), src.data_ptr(), dst.data_ptr(), src.shape[0],
-                                          _stream(stream))
+    d = _current(where, src)
+    if layers.device != d:
+        _refuse(where, f"the pool is on cuda:{layers.device}, src on cuda:{d}")
+    n = len(src) if src.dim() == 1 else -1
+    st = load_library().nf_kv_copy_blocks(layers.c, len(layers), _rows(where, "src", src, d, n), _rows(where, "dst", dst, d, n),
+                                          n, _stream(stream))
     _check(st, where)
 
 
@@ -584,16 +616,13 @@ def nf_kv_fork(layers: KVLayers, refs, block_table, src_rows, dst_rows, seqlens,
     pages are shared, a partly filled last page is copied in every layer, and
     seqlens[dst] = seqlens[src]."""
     where = "nf_kv_fork"
-    _pages_args(where, refs, block_table, ("seqlens",), src_rows=(src_rows, torch.int32),
-                dst_rows=(dst_rows, torch.int32), seqlens=(seqlens, torch.int32), workspace=(workspace, workspace.dtype))
-    if refs.shape[0] != layers.num_blocks or layers.device != refs.device:
-        _refuse(where, "refs must have one count per block of the pool, on its device")
-    if src_rows.dim() != 1 or src_rows.shape != dst_rows.shape:
-        _refuse(where, "src_rows and dst_rows must be [n]")
+    d = _pool_args(where, layers, refs, block_table, workspace)
+    rows, width = block_table.shape
+    n = len(src_rows) if src_rows.dim() == 1 else -1
     st = load_library().nf_kv_fork(
-        layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
-        src_rows.data_ptr(), dst_rows.data_ptr(), src_rows.shape[0], seqlens.data_ptr(), workspace.data_ptr(),
-        workspace.nbytes, _stream(stream))
+        layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), rows, width,
+        _rows(where, "src_rows", src_rows, d, n), _rows(where, "dst_rows", dst_rows, d, n), n,
+        _rows(where, "seqlens", seqlens, d, rows), workspace.data_ptr(), workspace.nbytes, _stream(stream))
     _check(st, where)
 
 
@@ -601,10 +630,8 @@ def nf_kv_compact(layers: KVLayers, refs, block_table, workspace, stream=None):
     """Move the blocks in use to the front of the pool, in every layer, and
     renumber the table (see nf.h)."""
     where = "nf_kv_compact"
-    _pages_args(where, refs, block_table, workspace=(workspace, workspace.dtype))
-    if refs.shape[0] != layers.num_blocks or layers.device != refs.device:
-        _refuse(where, "refs must have one count per block of the pool, on its device")
-    st = load_library().nf_kv_compact(
-        layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
-        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _pool_args(where, layers, refs, block_table, workspace)
+    rows, width = block_table.shape
+    st = load_library().nf_kv_compact(layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), rows, width,
+                                      workspace.data_ptr(), workspace.nbytes, _stream(stream))
     _check(st, where)

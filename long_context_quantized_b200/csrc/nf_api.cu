@@ -745,6 +745,30 @@ nf_status launch(const char *what, void (*kernel)(Params), unsigned grid, unsign
     return after_launch(what);
 }
 
+template <bool F32, bool PAIRS>
+cudaError_t launch_rope(const nf::RopeParams &p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.a.n_new, (unsigned)p.slices, (unsigned)p.a.batch);
+    cfg.blockDim = dim3(nf::kRopeWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (p.a.fmt) {
+        case NF_KV_K8V4: return cudaLaunchKernelEx(&cfg, nf::rope_append_kernel<F32, PAIRS, NF_KV_K8V4>, p);
+        case NF_KV_K8V8: return cudaLaunchKernelEx(&cfg, nf::rope_append_kernel<F32, PAIRS, NF_KV_K8V8>, p);
+        case NF_KV_F8: return cudaLaunchKernelEx(&cfg, nf::rope_append_kernel<F32, PAIRS, NF_KV_F8>, p);
+        case NF_KV_K4V4: return cudaLaunchKernelEx(&cfg, nf::rope_append_kernel<F32, PAIRS, NF_KV_K4V4>, p);
+        default: return cudaLaunchKernelEx(&cfg, nf::rope_append_kernel<F32, PAIRS, NF_KV_BF16>, p);
+    }
+}
+cudaError_t dispatch_rope(const nf::RopeParams &p, cudaStream_t s) {
+    return p.a.in_f32 ? (p.pairs ? launch_rope<true, true>(p, s) : launch_rope<true, false>(p, s))
+                      : (p.pairs ? launch_rope<false, true>(p, s) : launch_rope<false, false>(p, s));
+}
+
 nf_status done() {
     g_msg[0] = '\0';
     return NF_OK;
@@ -831,9 +855,9 @@ nf_status nf_rope_append_quant(const nf_kv_layer *kv, const nf_rope *rope, const
         return fail(NF_ERR_INVALID_ARG, "q_out must be %zu-byte aligned", align);
     const long long tokens = (long long)batch * n_new;
     const long long total = (long long)num_q_heads + 2ll * kv->num_kv_heads;
-    const long long most = (total + nf::kRopeWarps - 1) / nf::kRopeWarps;  // one row per warp
-    if (tokens > 0x7fffffffLL || total > 0x7fffffffLL)
+    if (tokens > 0x7fffffffLL || num_q_heads > (1 << 20) || kv->num_kv_heads > (1 << 20))
         return fail(NF_ERR_INVALID_ARG, "too many tokens or heads in one append");
+    if (batch > 65535) return fail(NF_ERR_UNSUPPORTED, "batch %d above 65535", batch);
     const int sms = current_sm_count();
     if (sms < 1) return fail(NF_ERR_CUDA, "cannot query the current device");
 
@@ -868,14 +892,18 @@ nf_status nf_rope_append_quant(const nf_kv_layer *kv, const nf_rope *rope, const
     p.inv_freq = rope->inv_freq;
     p.rot = rope->rot_dim;
     p.pairs = rope->layout == NF_ROPE_PAIRS;
-    for (int i = 0; i < rope->rot_dim / 2; ++i) p.axis[i] = rope->axis[i];
-    long long slices = (2ll * sms + tokens - 1) / tokens;
+    for (int i = 0; i < rope->rot_dim / 2; ++i) p.axis[i >> 4] |= (uint32_t)rope->axis[i] << (2 * (i & 15));
+    // few tokens: a token's rows over several CTAs, down to two rows a warp
+    const long long most = (total + 2 * nf::kRopeWarps - 1) / (2 * nf::kRopeWarps);
+    long long slices = sms / tokens;
     if (slices > most) slices = most;
-    if (slices < 1) slices = 1;  // (more than one only below 2 x SMs tokens: the grid stays below 2^31)
-    p.rows_per_slice = (int)((total + slices - 1) / slices);
-    p.slices = (int)((total + p.rows_per_slice - 1) / p.rows_per_slice);
-    return launch("rotary append kernel", nf::rope_append_kernel, (unsigned)(tokens * p.slices), nf::kRopeWarps * 32,
-                  stream, p);
+    p.slices = (int)(slices < 1 ? 1 : slices);
+    const cudaError_t e = dispatch_rope(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return fail(NF_ERR_CUDA, "rotary append kernel launch: %s", cudaGetErrorString(e));
+    }
+    return after_launch("rotary append kernel launch");
 }
 
 // ---------------------------------------------------------------- pages

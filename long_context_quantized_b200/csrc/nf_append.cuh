@@ -10,8 +10,9 @@
 // fp8 dtype (--kv-dtype fp8) stores e4m3 codes of x / (absmax / 448) for both;
 // the RK4V4-E8 reading (page "影片筆記：NInfer + 千问3.8 27b = 1.5倍速@256K上下文",
 // section 三) stores 4-bit codes of both with a power-of-two scale per 32 channels.
-// Division and rounding are the IEEE fp32 ones (__fdiv_rn, round half to even),
-// subnormals kept, so the codes are bit-identical to the format definition.
+// Division and rounding are the IEEE fp32 ones (or proven to give the same code,
+// see make_codes), round half to even, subnormals kept, so the codes are
+// bit-identical to the format definition.
 #pragma once
 
 #include "nf_common.cuh"
@@ -57,10 +58,41 @@ __device__ __forceinline__ __half make_scale(float a, float q, float &sigma) {
     return s16;
 }
 
-__device__ __forceinline__ int make_code(float x, float sigma, int q) {
-    if (sigma == 0.0f) return 0;
-    const int c = __float2int_rn(__fdiv_rn(x, sigma));  // round half to even
-    return min(max(c, -q), q);
+// Codes of four channels: round_half_even(fp32(x / sigma)) clamped to [-q, q], 0
+// when sigma is 0.  The IEEE quotient is only worked out where it matters: t =
+// x * rcp(sigma) is within 2^-22 of x / sigma relatively and the fp32 quotient
+// within 2^-24, so for |t| <= 128 both lie within 2^-14 of each other, and where
+// t is further than 2^-13 from every border n + 1/2 the two round alike (beyond
+// 128 both are clamped).  About one warp in 30 has a lane that is closer and
+// divides.
+__device__ __forceinline__ void make_codes(const float (&x)[4], float sigma, int q, int (&code)[4]) {
+    const float r = sigma == 0.0f ? 0.0f : rcp_approx(sigma);  // sigma >= 2^-24: normal
+    float t[4];
+    bool sure = true;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        t[c] = x[c] * r;
+        sure = sure && fabsf(t[c] - rintf(t[c])) < 0.5f - 0x1p-13f;  // false for infinities and NaN too
+    }
+    if (!sure) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) t[c] = sigma == 0.0f ? 0.0f : __fdiv_rn(x[c], sigma);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) code[c] = min(max(__float2int_rn(t[c]), -q), q);
+}
+
+// Four int8 codes (absmax / 127 scale) in one word.
+__device__ __forceinline__ uint32_t pack_codes8(const float (&x)[4], float sigma) {
+    int code[4];
+    make_codes(x, sigma, 127, code);
+    return prmt(prmt((uint32_t)code[0], (uint32_t)code[1], 0x0040), prmt((uint32_t)code[2], (uint32_t)code[3], 0x0040),
+                0x5410);
+}
+// Four nibbles, channel 0 in the lowest.
+__device__ __forceinline__ uint32_t pack_codes4(const int (&code)[4]) {
+    return ((uint32_t)code[0] & 0xFu) | (((uint32_t)code[1] & 0xFu) << 4) | (((uint32_t)code[2] & 0xFu) << 8) |
+           (((uint32_t)code[3] & 0xFu) << 12);
 }
 
 // One 128-channel row held 4 channels per lane -> int8 codes (absmax / 127
@@ -71,11 +103,30 @@ __device__ __forceinline__ void quant_row8(const float (&x)[4], int lane, int8_t
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     float sigma;
     const __half h = make_scale(a, 127.0f, sigma);
-    uint32_t c8 = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) c8 |= (uint32_t)(make_code(x[c], sigma, 127) & 0xFF) << (8 * c);
-    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = c8;
+    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = pack_codes8(x, sigma);
     if (lane == 0) *scale = h;
+}
+
+// Four e4m3 codes (absmax / 448 scale) in one word.
+__device__ __forceinline__ uint32_t pack_codes_f8(const float (&x)[4], float sigma) {
+    // as make_codes: t is within 2^-22 of the fp32 quotient relatively (about 2
+    // fp32 steps); an e4m3 border of a normal result lies where the 20 fp32
+    // mantissa bits below the 3 kept ones are 0x80000, so outside 8 steps of it,
+    // and above the subnormal results, both round alike
+    const float r = sigma == 0.0f ? 0.0f : rcp_approx(sigma);
+    float t[4];
+    bool sure = true;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        t[c] = x[c] * r;
+        const uint32_t low = (__float_as_uint(t[c]) & 0xFFFFFu) - 0x80000u + 8u;
+        sure = sure && low > 16u && fabsf(t[c]) >= 0x1p-6f && fabsf(t[c]) < 512.0f;
+    }
+    if (!sure) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) t[c] = sigma == 0.0f ? 0.0f : __fdiv_rn(x[c], sigma);
+    }
+    return f32x4_to_e4m3(t[0], t[1], t[2], t[3]);
 }
 
 // The same row -> e4m3 codes of x / scale (scale absmax / 448), 0 when the
@@ -86,11 +137,26 @@ __device__ __forceinline__ void quant_row_f8(const float (&x)[4], int lane, uint
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     float sigma;
     const __half h = make_scale(a, 448.0f, sigma);
-    float t[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) t[c] = sigma == 0.0f ? 0.0f : __fdiv_rn(x[c], sigma);
-    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = f32x4_to_e4m3(t[0], t[1], t[2], t[3]);
+    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = pack_codes_f8(x, sigma);
     if (lane == 0) *scale = h;
+}
+
+// The exponent e of a group with absmax a (see quant_row_e8) and 2^-e.
+__device__ __forceinline__ int e8_exponent(float a, float &inv) {
+    const uint32_t sb = __float_as_uint(__fdiv_rn(a, 7.0f));
+    const int ef = (int)(sb >> 23);  // biased exponent; 0 for zero and subnormal quotients
+    int e = ef == 0 ? -126 : ef - 127 + ((sb & 0x7FFFFFu) != 0u ? 1 : 0);
+    e = min(max(e, -126), 127);
+    // x / 2^e = x * 2^-e exactly (2^-127 is a subnormal factor; a product below
+    // the normal range is rounded as the quotient would be)
+    inv = e == 127 ? 0x1p-127f : __int_as_float((127 - e) << 23);
+    return e;
+}
+__device__ __forceinline__ uint32_t pack_codes_e8(const float (&x)[4], float inv) {
+    int code[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) code[c] = min(max(__float2int_rn(x[c] * inv), -7), 7);
+    return pack_codes4(code);
 }
 
 // RK4V4-E8 (both K and V): one power-of-two scale 2^e per 32 channels = 8
@@ -103,18 +169,9 @@ __device__ __forceinline__ void quant_row_e8(const float (&x)[4], int lane, uint
     float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const uint32_t sb = __float_as_uint(__fdiv_rn(a, 7.0f));
-    const int ef = (int)(sb >> 23);  // biased exponent; 0 for zero and subnormal quotients
-    int e = ef == 0 ? -126 : ef - 127 + ((sb & 0x7FFFFFu) != 0u ? 1 : 0);
-    e = min(max(e, -126), 127);
-    const float scale = __int_as_float((e + 127) << 23);
-    uint32_t c4 = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int q = min(max(__float2int_rn(__fdiv_rn(x[c], scale)), -7), 7);
-        c4 |= (uint32_t)(q & 0xF) << (4 * c);
-    }
-    *reinterpret_cast<uint16_t *>(codes + 2 * lane) = (uint16_t)c4;
+    float inv;
+    const int e = e8_exponent(a, inv);
+    *reinterpret_cast<uint16_t *>(codes + 2 * lane) = (uint16_t)pack_codes_e8(x, inv);
     if ((lane & 7) == 0) scales[lane >> 3] = (uint8_t)(e + 127);
 }
 
@@ -160,11 +217,10 @@ __device__ __forceinline__ void store_v_row(const AppendParams &p, const float (
     for (int o = 4; o > 0; o >>= 1) av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
     float sv;
     const __half hv = make_scale(av, 7.0f, sv);
-    uint32_t vc = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) vc |= (uint32_t)(make_code(v[c], sv, 7) & 0xF) << (4 * c);
+    int code[4];
+    make_codes(v, sv, 7, code);
     *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.v_codes) + si * (kHeadDim / 2) + 2 * lane) =
-        (uint16_t)vc;
+        (uint16_t)pack_codes4(code);
     if ((lane & 7) == 0) p.v_scales[si * (kHeadDim / kVGroup) + (lane >> 3)] = hv;
 }
 
