@@ -24,6 +24,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-shared",
     # IEEE division and denormals: the quantiser must match the format bit for bit
     "-prec-div=true", "-ftz=false", "-fmad=true",
+    "--split-compile=0",  # optimise the many instantiations on all cores
 ]
 
 

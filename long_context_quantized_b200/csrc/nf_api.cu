@@ -195,7 +195,7 @@ cudaError_t launch_decode(const nf::DecodeParams &p, int ctas, cudaStream_t s) {
 
 // The tensor-core decode of many rows (K8/V4 or K8V8, 9 to 32 query rows per
 // kv-head), rows padded to RP = 16 or 32.
-template <int RP, bool QF32, int FMT>
+template <int RP, bool QF32, int FMT, bool WIN>
 cudaError_t launch_decode_tc(const nf::DecodeParams &p, int ctas, cudaStream_t s) {
     constexpr int smem = nf::DtSmem<FMT>::kBytes;
     static std::atomic<uint64_t> opted{0};
@@ -204,16 +204,24 @@ cudaError_t launch_decode_tc(const nf::DecodeParams &p, int ctas, cudaStream_t s
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(opted.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(nf::decode_tc_kernel<RP, QF32, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(nf::decode_tc_kernel<RP, QF32, FMT, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         opted.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_pdl(nf::decode_tc_kernel<RP, QF32, FMT>, (unsigned)ctas, nf::kDtThreads, smem, s, p);
+    return launch_pdl(nf::decode_tc_kernel<RP, QF32, FMT, WIN>, (unsigned)ctas, nf::kDtThreads, smem, s, p);
 }
-template <int FMT>
-cudaError_t dispatch_decode_tc(const nf::DecodeParams &p, bool qf32, int rows, int ctas, cudaStream_t s) {
-    return rows <= 16 ? (qf32 ? launch_decode_tc<16, true, FMT>(p, ctas, s) : launch_decode_tc<16, false, FMT>(p, ctas, s))
-                      : (qf32 ? launch_decode_tc<32, true, FMT>(p, ctas, s) : launch_decode_tc<32, false, FMT>(p, ctas, s));
+template <int FMT, bool WIN>
+cudaError_t dispatch_decode_tc_q(const nf::DecodeParams &p, bool qf32, int rows, int ctas, cudaStream_t s) {
+    return rows <= 16 ? (qf32 ? launch_decode_tc<16, true, FMT, WIN>(p, ctas, s)
+                              : launch_decode_tc<16, false, FMT, WIN>(p, ctas, s))
+                      : (qf32 ? launch_decode_tc<32, true, FMT, WIN>(p, ctas, s)
+                              : launch_decode_tc<32, false, FMT, WIN>(p, ctas, s));
+}
+template <bool WIN>
+cudaError_t dispatch_decode_tc(const nf::DecodeParams &p, bool qf32, int fmt, int rows, int ctas, cudaStream_t s) {
+    return fmt == NF_KV_K8V8 ? dispatch_decode_tc_q<NF_KV_K8V8, WIN>(p, qf32, rows, ctas, s)
+           : fmt == NF_KV_F8 ? dispatch_decode_tc_q<NF_KV_F8, WIN>(p, qf32, rows, ctas, s)
+                             : dispatch_decode_tc_q<NF_KV_K8V4, WIN>(p, qf32, rows, ctas, s);
 }
 
 bool uses_decode_tc(int fmt, int rows) {
@@ -331,7 +339,7 @@ nf_status run_decode(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int3
         return fail(NF_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
 
     nf::DecodeParams p{};
-    const bool tc = !win && uses_decode_tc(kv->fmt, pl.rows);
+    const bool tc = uses_decode_tc(kv->fmt, pl.rows);
     // decode_tc_kernel loads a tile's K and V rows with one box each
     const unsigned box_rows = tc ? (unsigned)nf::kDtTileKeys : (unsigned)nf::kChunk;
     if (kv->fmt != NF_KV_BF16) {
@@ -388,9 +396,8 @@ nf_status run_decode(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int3
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool qf32 = q_dtype == NF_F32;
     const cudaError_t e =
-        tc ? (kv->fmt == NF_KV_K8V8 ? dispatch_decode_tc<NF_KV_K8V8>(p, qf32, pl.rows, pl.ctas, s)
-              : kv->fmt == NF_KV_F8 ? dispatch_decode_tc<NF_KV_F8>(p, qf32, pl.rows, pl.ctas, s)
-                                    : dispatch_decode_tc<NF_KV_K8V4>(p, qf32, pl.rows, pl.ctas, s))
+        tc ? (win ? dispatch_decode_tc<true>(p, qf32, kv->fmt, pl.rows, pl.ctas, s)
+                  : dispatch_decode_tc<false>(p, qf32, kv->fmt, pl.rows, pl.ctas, s))
         : win ? (pl.nt == 1 ? dispatch_decode<1, true>(p, qf32, kv->fmt, pl.ctas, s)
                             : dispatch_decode<2, true>(p, qf32, kv->fmt, pl.ctas, s))
               : (pl.nt == 1 ? dispatch_decode<1, false>(p, qf32, kv->fmt, pl.ctas, s)

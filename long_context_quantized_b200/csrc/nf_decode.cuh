@@ -217,6 +217,15 @@ __device__ __forceinline__ void store_out4(float *out, int bf16, size_t row, int
         reinterpret_cast<float4 *>(out + row * kHeadDim)[c4] = o;
 }
 
+// One output channel likewise.
+template <bool WIN>
+__device__ __forceinline__ void store_out1(float *out, int bf16, size_t at, float v) {
+    if (WIN && bf16)
+        reinterpret_cast<__nv_bfloat16 *>(out)[at] = __float2bfloat16_rn(v);
+    else
+        out[at] = v;
+}
+
 template <int NT, int FMT>
 struct DecodeSmem {
     static constexpr int NR = NT * 8;
@@ -698,7 +707,7 @@ constexpr uint64_t kCoopWaitNs = 50000ull;
 // partial sums are then added in order, so the arithmetic depends only on (n,
 // m, j, rows), not on which CTA merges the share.  A row no piece saw a key
 // of (every lse -inf) comes out as o = 0, lse = -inf.
-template <int NTHR, uint32_t BAR>
+template <int NTHR, uint32_t BAR, bool WIN>
 __device__ __forceinline__ void merge_share(const DecodeParams &p, const float *slots, int n, int rows, int j, int m,
                                             float *sm, int b, int h) {
     constexpr float kLog2e = 1.4426950408889634f;
@@ -787,7 +796,7 @@ __device__ __forceinline__ void merge_share(const DecodeParams &p, const float *
             const int ri = (c0 + tid) / 32, ci = (c0 + tid) % 32;
             const int jq = ri / p.group, gq = ri % p.group;
             const size_t row = ((size_t)b * p.n_q + jq) * p.num_q_heads + (size_t)h * p.group + gq;
-            reinterpret_cast<float4 *>(p.out + row * kHeadDim)[ci] = sum;
+            store_out4<WIN>(p.out, p.out_bf16, row, ci, sum);
         }
         named_sync(BAR, NTHR);  // the scratch is free again
     }
@@ -965,7 +974,7 @@ __device__ __forceinline__ void finish_piece_single(const DecodeParams &p, int s
 //    the done count and the share flags to zero for the next call.
 // No wait is unbounded, and a CTA that stops waiting loses nothing: its share
 // is swept by the last ticket's CTA.
-template <int NTHR, uint32_t BAR>
+template <int NTHR, uint32_t BAR, bool WIN>
 __device__ __forceinline__ void finish_piece_coop(const DecodeParams &p, int s_id, int first, int k, int n, int m,
                                                      float *sm, volatile int *misc, int rows, int b, int h) {
     constexpr int NW = NTHR / 32;
@@ -983,14 +992,14 @@ __device__ __forceinline__ void finish_piece_coop(const DecodeParams &p, int s_i
         misc[2] = ready && k < m && atomicCAS(&flag[k], 0, 1) == 0;
     }
     named_sync(BAR, NTHR);
-    if (misc[2]) merge_share<NTHR, BAR>(p, slots, n, rows, k, m, sm, b, h);
+    if (misc[2]) merge_share<NTHR, BAR, WIN>(p, slots, n, rows, k, m, sm, b, h);
     if (misc[1]) {
         // the sweep: the shares nobody has claimed
         int *won = reinterpret_cast<int *>(sm + (NW + 2) * kMaxCtas + 4 * NTHR);
         if ((int)threadIdx.x < m) won[threadIdx.x] = atomicCAS(&flag[threadIdx.x], 0, 1) == 0;
         named_sync(BAR, NTHR);
         for (int j = 0; j < m; ++j)
-            if (won[j]) merge_share<NTHR, BAR>(p, slots, n, rows, j, m, sm, b, h);
+            if (won[j]) merge_share<NTHR, BAR, WIN>(p, slots, n, rows, j, m, sm, b, h);
     }
     named_sync(BAR, NTHR);  // this CTA's merge reads and writes precede its done count
     if (threadIdx.x == 0 && atomic_add_acq_rel(&p.done[s_id], 1) == n - 1) {
@@ -1204,10 +1213,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
             const int r = idx / kHeadDim, ch = idx % kHeadDim;
             const int j = r / p.group, gq = r % p.group;
             const size_t row = ((size_t)b * p.n_q + j) * p.num_q_heads + (size_t)h * p.group + gq;
-            if (WIN && p.out_bf16)
-                reinterpret_cast<__nv_bfloat16 *>(p.out)[row * kHeadDim + ch] = __float2bfloat16_rn(0.f);
-            else
-                p.out[row * kHeadDim + ch] = 0.f;
+            store_out1<WIN>(p.out, p.out_bf16, row * kHeadDim + ch, 0.f);
             if (ch == 0 && p.out_lse) p.out_lse[row] = -INFINITY;
         }
     }

@@ -168,6 +168,18 @@ __device__ __forceinline__ int dt_tile_end(int cx, int cx_end) {
     return min(cx_end, min((cx / kDtChunkTiles + 1) * kDtChunkTiles, cx + 128 / kChunk));
 }
 
+// One tile of a sequence's chunk list: the list position cx is chunk cx (WIN: cx
+// or cx + skip, see win_span); returns the position behind the tile and gives
+// its first key and number of keys.
+template <bool WIN>
+__device__ __forceinline__ int dt_tile(int cx, int cx1, const WinSpan &span, int &tok0, int &ntok) {
+    const int off = WIN && cx >= span.sinks ? span.skip : 0;
+    const int ce = dt_tile_end(cx + off, (WIN && cx < span.sinks ? min(cx1, span.sinks) : cx1) + off);
+    tok0 = (cx + off) * kChunk;
+    ntok = (ce - cx - off) * kChunk;
+    return ce - off;
+}
+
 // The largest exponent field E (at least 1) of a key's four fp16 V scales:
 // V' = code x scale x 2^(15 - E) and f = 2^(E - 15) (both sides must agree).
 __device__ __forceinline__ int dt_v_exponent(uint2 vs) {
@@ -220,7 +232,8 @@ __device__ __forceinline__ void dt_st(uint32_t taddr, const uint32_t (&r)[HR]) {
 // no max yet, so one FMA per score gives the exponent y = x - m - kLazy (a
 // score's x = v c with v its integer dot product and c the row's and key's
 // factors) and y > 0 flags a score above the threshold.
-// FAST: every row sees every key of the tile (no mask).
+// FAST: every row sees every key of the tile (no mask); else the rows rmin .. R -
+// 1 see this thread's key (windowed: R is the key's own bound).
 // When the max rises and O^T holds earlier tiles of the piece (has_o), the
 // rows' columns of O^T (taddr) are scaled once the last P.V is done (pv_bar).
 // The raw product of a row and key from the S words: int8 digits S1 * 254 +
@@ -310,7 +323,8 @@ __device__ __forceinline__ void dt_softmax(const uint32_t (&d1)[HR], const uint3
     }
 }
 
-template <int RP, bool QF32, int FMT>
+// WIN: the windowed form, as decode_kernel's.
+template <int RP, bool QF32, int FMT, bool WIN>
 __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_constant__ DecodeParams p) {
     static_assert(RP == 16 || RP == 32, "rows padded to 16 or 32");
     static_assert(FMT == NF_KV_K8V4 || FMT == NF_KV_K8V8 || FMT == NF_KV_F8, "int8 or e4m3 K codes");
@@ -381,8 +395,8 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
         for (int b = lane; b < p.batch; b += 32) {
             const int L = p.seqlens[b];
             const bool ok = L >= p.n_q && L <= p.max_seqlen;
-            if (!ok && blockIdx.x == 0) report(NF_DEVERR_SEQLEN);
-            seqC[b] = ok ? (L + kChunk - 1) / kChunk : 0;
+            if (!ok && blockIdx.x == 0 && !(WIN && L == 0)) report(NF_DEVERR_SEQLEN);
+            seqC[b] = ok ? (L + kChunk - 1) / kChunk - (WIN ? win_span(L, p.n_q, p.window, p.n_sink).skip : 0) : 0;
             seqL[b] = ok ? L : 0;
         }
         __syncwarp();
@@ -406,6 +420,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
     const long long c_begin = vb < P ? W * vb / P : 0;
     const long long c_end = vb < P ? W * (vb + 1) / P : 0;
     PieceWalker walk{seqC, seqBase, H, p.batch, kDtSegPad, c_begin, c_end};
+    auto span_of = [&](int b) { return WIN ? win_span(seqL[b], p.n_q, p.window, p.n_sink) : WinSpan{0, 0, 0}; };
 
     if (warp == kDtProducer) {
         // =============================================================== producer
@@ -414,13 +429,13 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
         bool waited = !p.early_kv;
         while (!stop && walk.next()) {
             const int32_t *bt = p.block_table + (size_t)walk.pb * p.max_blocks;
-            const int nblk = (seqC[walk.pb] * kChunk + kBlock - 1) / kBlock;
+            const WinSpan span = span_of(walk.pb);
+            const int nblk = ((seqC[walk.pb] + span.skip) * kChunk + kBlock - 1) / kBlock;
             int win = -1000000, my_blk = 0;
             const int cx1 = (int)(walk.xe - walk.s0);
             for (int cx = (int)(walk.xs - walk.s0); cx < cx1; ++kst) {
-                const int ce = dt_tile_end(cx, cx1);
-                const int tok0 = cx * kChunk, ntok = (ce - cx) * kChunk;
-                cx = ce;
+                int tok0, ntok;
+                cx = dt_tile<WIN>(cx, cx1, span, tok0, ntok);
                 if (!waited && tok0 + ntok > seqL[walk.pb] - p.n_q) {
                     pdl_wait();  // the newest rows may come from the kernels before this one
                     waited = true;
@@ -479,9 +494,11 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
             while (!misc[0] && walk.next()) {
                 dt_wait(&qfull[pc & 1], (pc >> 1) & 1, misc);
                 const uint32_t qaddr = sQ + (pc & 1) * (uint32_t)SM::kQBuf;
+                const WinSpan span = span_of(walk.pb);
                 const int cx1 = (int)(walk.xe - walk.s0);
                 for (int cx = (int)(walk.xs - walk.s0); cx < cx1 && !misc[0]; ++kt) {
-                    cx = dt_tile_end(cx, cx1);
+                    int tok0, ntok;
+                    cx = dt_tile<WIN>(cx, cx1, span, tok0, ntok);
                     const uint32_t stage = kt % NS, sb = kt & 1;
                     dt_wait(&full[stage], (kt / NS) & 1, misc);
                     dt_wait(&sfree[sb], ((kt >> 1) & 1) ^ 1, misc);
@@ -515,10 +532,12 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
             const uint32_t sVh = smem_addr(smem + SM::kVh), sP = smem_addr(smem + SM::kP);
             uint32_t pj = 0;
             while (!misc[0] && walk.next()) {
+                const WinSpan span = span_of(walk.pb);
                 const int cx1 = (int)(walk.xe - walk.s0);
                 bool ovw = true;
                 for (int cx = (int)(walk.xs - walk.s0); cx < cx1 && !misc[0]; ++pj) {
-                    cx = dt_tile_end(cx, cx1);
+                    int tok0, ntok;
+                    cx = dt_tile<WIN>(cx, cx1, span, tok0, ntok);
                     const uint32_t b = pj & 1;
                     if (b == mine) {
                         dt_wait(&pfull[b], (pj >> 1) & 1, misc);
@@ -566,7 +585,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
                 const int r = idx / kHeadDim, ch = idx % kHeadDim;
                 const int j = r / p.group, gq = r % p.group;
                 const size_t row = ((size_t)b * p.n_q + j) * p.num_q_heads + (size_t)h * p.group + gq;
-                p.out[row * kHeadDim + ch] = 0.f;
+                store_out1<WIN>(p.out, p.out_bf16, row * kHeadDim + ch, 0.f);
                 if (ch == 0 && p.out_lse) p.out_lse[row] = -INFINITY;
             }
         }
@@ -672,12 +691,12 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
             // causal: key position pos is seen by rows r >= (pos - (L - n_q)) * G
             const int causal_base = p.causal ? L - p.n_q : 0x7fffffff;
             const int all_see = p.causal ? L - p.n_q + 1 : L;  // keys every row sees
+            const WinSpan span = span_of(b);
             const uint32_t kfirst = kt;
             const int cx1 = pce.cx1;
             for (int cx = pce.cx0; cx < cx1; ++kt) {
-                const int ce = dt_tile_end(cx, cx1);
-                const int tok0 = cx * kChunk, ntok = (ce - cx) * kChunk;
-                cx = ce;
+                int tok0, ntok;
+                cx = dt_tile<WIN>(cx, cx1, span, tok0, ntok);
                 const uint32_t stage = kt % NS, sb = kt & 1;
                 const unsigned char *st = smem + stage * SM::kStride;
                 // ---- the stage: this key's V nibbles of group hq, its scales;
@@ -685,8 +704,10 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
                 dt_wait(&full[stage], (kt / NS) & 1, misc);
                 const int pos = tok0 + i;
                 const bool sok = stage_ok[stage] != 0;  // (garbage after an abort is never used)
-                const bool kv_ok = sok && i < ntok && pos < L;
-                const bool fast = sok && ntok == 128 && tok0 + 128 <= all_see && R == RP;
+                // (windowed: a key that some row sees; the others' bytes stay out)
+                const bool kv_ok = sok && i < ntok && pos < L && (!WIN || pos >= span.lo || pos < p.n_sink);
+                const bool fast = sok && ntok == 128 && tok0 + 128 <= all_see && R == RP &&
+                                  (!WIN || tok0 + 128 <= p.n_sink || tok0 >= L - p.window);
                 // K8/V4: the group's 16 bytes of nibbles; K8V8: its 32 bytes of codes
                 constexpr int VW = V8 ? 2 : 1;
                 uint4 nib[kDtVG][VW];
@@ -787,14 +808,16 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
                 mbar_arrive(&sfree[sb]);
                 const int dpos = pos - causal_base;
                 const int rmin = kv_ok ? (dpos > 0 ? dpos * p.group : 0) : 0x7fffffff;  // rows rmin .. R - 1 see it
+                // windowed: behind row rend - 1 the key has left the window
+                const int rend = !WIN || pos < p.n_sink ? R : (int)min((long long)R, (long long)(dpos + p.window) * p.group);
                 const float f = __int_as_float((127 + ev - 15) << 23);
                 uint32_t pk[HR / 2];
                 const uint32_t ota = tmem + lane_base + kOCol + r0;
                 if (fast)
-                    dt_softmax<HR, true, F8>(d1, d2, d3, qwr, ksv, rmin, R, r0, nthr, l_part, red, qd, lane, gbar, f, pk,
+                    dt_softmax<HR, true, F8>(d1, d2, d3, qwr, ksv, rmin, rend, r0, nthr, l_part, red, qd, lane, gbar, f, pk,
                                          kt > kfirst, ota, &pvdone[(kt - 1) & 1], ((kt - 1) >> 1) & 1, misc);
                 else
-                    dt_softmax<HR, false, F8>(d1, d2, d3, qwr, ksv, rmin, R, r0, nthr, l_part, red, qd, lane, gbar, f, pk,
+                    dt_softmax<HR, false, F8>(d1, d2, d3, qwr, ksv, rmin, rend, r0, nthr, l_part, red, qd, lane, gbar, f, pk,
                                           kt > kfirst, ota, &pvdone[(kt - 1) & 1], ((kt - 1) >> 1) & 1, misc);
                 // P' row of this key, rows r0 .. r0 + HR - 1 (half of one, one or two
                 // 16-byte chunks)
@@ -849,7 +872,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
                                                                (size_t)h * p.group + r % p.group
                                                          : 0;
                         if (n_pieces == 1)
-                            p.out[row * kHeadDim + ch] = val;
+                            store_out1<WIN>(p.out, p.out_bf16, row * kHeadDim + ch, val);
                         else
                             slotp[r * kHeadDim + ch] = val;
                         if (i == e0 + e) {  // one lane per row: the row's lse
@@ -864,7 +887,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
                 tc_fence_before();
             }
             named_sync(kDtBarAll, kDtConsumers * 32);  // the piece's outputs are written
-            finish_piece_coop<kDtConsumers * 32, kDtBarAll>(p, s_id, first, vb - first, n_pieces, pce.m,
+            finish_piece_coop<kDtConsumers * 32, kDtBarAll, WIN>(p, s_id, first, vb - first, n_pieces, pce.m,
                                                                reinterpret_cast<float *>(smem + SM::kVh), misc, R, b,
                                                                h);
             named_sync(kDtBarAll, kDtConsumers * 32);  // the merge is done: its buffers are free again

@@ -86,7 +86,21 @@ def window_attention(kv, q, table, seqlens, window, n_sink, scale):
                     spread[b, j, g] = len(s) / e.sum() * np.abs(vv).max()
                     dq[b, j, g] = scale * np.abs(q[b, j, g]).max() * np.abs(kk).sum(1).max()
                     dk[b, j, g] = scale * (np.abs(kk) @ np.abs(q[b, j, g])).max()
-    return out, lse, dict(mag=mag, spread=spread, dq=dq, dk=dk)
+    return out, lse, dict(mag=mag, spread=spread, dq=dq, dk=dk, lift=value_lift(kv, G * n_q))
+
+
+def value_lift(kv, rows):
+    """9 to 32 rows of K8/V4, int8 and fp8 pools run on tcgen05, where a weight
+    is multiplied by 2^(E - 15), E the exponent field of the key's largest V
+    scale, and its value by the inverse: the largest 2^(15 - E) of the pool's
+    slots.  1 for the other shapes."""
+    if kv.fmt not in (nf.NF_KV_K8V4, nf.NF_KV_K8V8, nf.NF_KV_F8) or not 9 <= rows <= 32:
+        return 1.0
+    bits = kv.v_scales.view(torch.int16).cpu().numpy().astype(np.int64) & 0x7FFF
+    field = bits >> 10
+    if kv.fmt == nf.NF_KV_K8V4:
+        field = field.max(-1)
+    return float(2.0 ** (15 - max(1, int(field[(bits > 0).any(-1) if bits.ndim > field.ndim else bits > 0].min()))))
 
 
 def decode_tolerance(parts):
@@ -96,12 +110,13 @@ def decode_tolerance(parts):
     2^-11 relative, of sum w |v|.  A weight (or product) below fp16's normal
     range 2^-14 is off by at most 2^-25 instead, where the largest weight is at
     least 2^-4, so the row sum is at least sum exp(s - max) / 16: n 2^-25 16 /
-    sum exp(s - max) x max|v|, twice (weight and product).  The query's two
+    sum exp(s - max) x max|v|, twice (weight and product) -- times the lift 2^(15
+    - E) that the tcgen05 form takes out of the weights.  The query's two
     digits leave 2^-16 max|q| per element, which moves a score by at most dq
     2^-16 and a normalised weight by twice that relatively.  fp32 sums and
     exponentials: 2^-15 covers 2^8 additions of half a step each, and the
     conversions."""
-    return (2.0 ** -10 + 2 * 2.0 ** -16 * parts["dq"] + 2.0 ** -15) * parts["mag"] + parts["spread"] * 2.0 ** -20
+    return (2.0 ** -10 + 2 * 2.0 ** -16 * parts["dq"] + 2.0 ** -15) * parts["mag"] + parts["spread"] * 2.0 ** -20 * parts["lift"]
 
 
 def prefill_tolerance(parts):

@@ -122,11 +122,12 @@ def test_decode_window_long_splits():
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_decode_window_bytes_of_hidden_keys_do_not_matter(fmt):
+@pytest.mark.parametrize("hq", [4, 8, 20])
+def test_decode_window_bytes_of_hidden_keys_do_not_matter(fmt, hq):
     """Pages out of every window may be gone, and hidden keys that share a page
     (and a chunk) with seen ones may hold anything, not-a-number included."""
     window, n_sink, n_q = 300, 5, 3
-    c = Case(fmt, [1400, 800], n_q=n_q)
+    c = Case(fmt, [1400, 800], n_q=n_q, hq=hq)
     want = c.check(window, n_sink)
     for b, L in enumerate(c.seqlens):
         first = L - n_q - window + 1
@@ -144,10 +145,10 @@ def test_decode_window_bytes_of_hidden_keys_do_not_matter(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_decode_window_of_everything_is_causal_attention(fmt):
-    """With a window of at least the length the call is nf_decode_attn, bit for
-    bit (at most 8 rows a kv-head, where both run the same kernel)."""
-    c = Case(fmt, [2500, 513], n_q=2, hq=8, hkv=2)
+@pytest.mark.parametrize("n_q, hq, hkv", [(2, 8, 2), (3, 8, 2), (4, 8, 1), (8, 8, 1)])
+def test_decode_window_of_everything_is_causal_attention(fmt, n_q, hq, hkv):
+    """With a window of at least the length the call is nf_decode_attn, bit for bit."""
+    c = Case(fmt, [2500, 513], n_q=n_q, hq=hq, hkv=hkv)
     got = c.run(2500, 0)
     out = torch.empty_like(got)
     nf.nf_decode_attn(c.kv, c.q, c.table, c.lens, c.max_len, SCALE, True, out, None, c.ws)
