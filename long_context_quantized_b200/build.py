@@ -15,7 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnf.so")
 SOURCES = ["nf_api.cu"]
 HEADERS = ["nf_common.cuh", "nf_append.cuh", "nf_decode.cuh", "nf_decode_tc.cuh", "nf_combine.cuh", "nf_prefill.cuh",
-           "nf_tc.cuh", "nf_rope.cuh", "nf_pages.cuh"]
+           "nf_prefill_win.cuh", "nf_tc.cuh", "nf_rope.cuh", "nf_pages.cuh"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
@@ -24,7 +24,6 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-shared",
     # IEEE division and denormals: the quantiser must match the format bit for bit
     "-prec-div=true", "-ftz=false", "-fmad=true",
-    "--split-compile=0",  # optimise the many instantiations on all cores
 ]
 
 

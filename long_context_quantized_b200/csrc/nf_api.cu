@@ -17,6 +17,7 @@
 #include "nf_decode_tc.cuh"
 #include "nf_pages.cuh"
 #include "nf_prefill.cuh"
+#include "nf_prefill_win.cuh"
 #include "nf_rope.cuh"
 
 namespace nf {
@@ -637,7 +638,7 @@ nf_status run_prefill(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int
     if (rows > 0x7fffffffLL || row_tiles > 0x7fffffffLL)
         return fail(NF_ERR_UNSUPPORTED, "prefill: %lld query rows per kv-head", rows);
 
-    nf::PrefillParams p{};
+    nf::PrefillWinParams p{};
     p.k_codes = static_cast<const int8_t *>(kv->k_codes);
     p.k_scales = static_cast<const __half *>(kv->k_scales);
     p.v_codes = static_cast<const uint8_t *>(kv->v_codes);
@@ -665,21 +666,22 @@ nf_status run_prefill(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int
         p.out_bf16 = win->out_bf16;
     }
 
-    st = win ? opt_in_smem<nf::prefill_tc_kernel<true>>(nf::TcSmem::kBytes)
-             : opt_in_smem<nf::prefill_tc_kernel<false>>(nf::TcSmem::kBytes);
+    st = win ? opt_in_smem<nf::prefill_win_kernel>(nf::PwSmem::kBytes)
+             : opt_in_smem<nf::prefill_tc_kernel>(nf::TcSmem::kBytes);
     if (st != NF_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)row_tiles, (unsigned)kv->num_kv_heads, (unsigned)batch);
-    cfg.blockDim = dim3(nf::kTcThreads);
-    cfg.dynamicSmemBytes = nf::TcSmem::kBytes;
+    static_assert(nf::kTcRows == nf::kPwRows, "both forms take 256 rows per CTA");
+    cfg.blockDim = dim3(win ? nf::kPwThreads : nf::kTcThreads);
+    cfg.dynamicSmemBytes = win ? nf::PwSmem::kBytes : nf::TcSmem::kBytes;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = win ? cudaLaunchKernelEx(&cfg, nf::prefill_tc_kernel<true>, p)
-                              : cudaLaunchKernelEx(&cfg, nf::prefill_tc_kernel<false>, p);
+    const cudaError_t e = win ? cudaLaunchKernelEx(&cfg, nf::prefill_win_kernel, p)
+                              : cudaLaunchKernelEx(&cfg, nf::prefill_tc_kernel, static_cast<const nf::PrefillParams &>(p));
     if (e != cudaSuccess) {
         (void)cudaGetLastError();  // a refused launch leaves no sticky state for the next call
         return fail(NF_ERR_CUDA, "prefill kernel launch: %s", cudaGetErrorString(e));

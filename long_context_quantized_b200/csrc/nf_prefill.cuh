@@ -40,9 +40,6 @@ struct PrefillParams {
     int causal;
     float *out;      // [batch][n_q][H_q][128]
     float *out_lse;  // [batch][n_q][H_q] or null
-    // windowed calls only: a query at position P sees keys t <= P with t > P - window or t < n_sink
-    int window, n_sink;
-    int out_bf16;  // out holds bf16 (o rounded once) instead of fp32
 };
 
 // ============================================================================
@@ -114,15 +111,7 @@ __device__ __forceinline__ uint32_t tc_swz(int r, int c, uint32_t blk) {
 struct TcRawK {
     uint4 k[8];   // K codes of the key
     uint32_t ks;  // K scale (low half)
-    int ok;       // key inside the sequence (windowed: seen by some row of the CTA)
-};
-// The keys [0, n_sink) and [lo, end) a CTA's rows see between them; a plain
-// causal or full call has n_sink = lo = 0, end = L.  tile j of the CTA's list
-// holds the 64 keys of key tile j + (j >= sinks ? skip : 0).
-struct TcKeys {
-    int n_sink, lo, end, sinks, skip;
-    __device__ __forceinline__ bool seen(int pos) const { return pos < end && (pos >= lo || pos < n_sink); }
-    __device__ __forceinline__ int tile(int j) const { return j + (j >= sinks ? skip : 0); }
+    int ok;       // key inside the sequence
 };
 struct TcRawV {
     uint4 v[4];   // V nibbles
@@ -141,13 +130,12 @@ __device__ __forceinline__ size_t tc_slot(const PrefillParams &p, const int32_t 
     }
     return ((size_t)blk * p.num_kv_heads + h) * kBlock + (pos & (kBlock - 1));
 }
-template <bool WIN>
-__device__ __forceinline__ void tc_load_k(const PrefillParams &p, const int32_t *bt, const TcKeys &keys, int h, int j,
-                                          int key, TcRawK &r) {
-    const int pos = (WIN ? keys.tile(j) : j) * kTcKeys + key;
+__device__ __forceinline__ void tc_load_k(const PrefillParams &p, const int32_t *bt, int L, int h, int tile, int key,
+                                          TcRawK &r) {
+    const int pos = tile * kTcKeys + key;
     bool good;
     const size_t si = tc_slot(p, bt, h, pos, good);
-    r.ok = good && (WIN ? keys.seen(pos) : pos < keys.end);
+    r.ok = good && pos < L;
     if (!good) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) r.k[u] = make_uint4(0, 0, 0, 0);
@@ -159,13 +147,12 @@ __device__ __forceinline__ void tc_load_k(const PrefillParams &p, const int32_t 
     for (int u = 0; u < 8; ++u) r.k[u] = ldg16(kp + 16 * u);
     r.ks = __ldg(reinterpret_cast<const unsigned short *>(p.k_scales + si));
 }
-template <bool WIN>
-__device__ __forceinline__ void tc_load_v(const PrefillParams &p, const int32_t *bt, const TcKeys &keys, int h, int j,
-                                          int key, TcRawV &r) {
-    const int pos = (WIN ? keys.tile(j) : j) * kTcKeys + key;
+__device__ __forceinline__ void tc_load_v(const PrefillParams &p, const int32_t *bt, int L, int h, int tile, int key,
+                                          TcRawV &r) {
+    const int pos = tile * kTcKeys + key;
     bool good;
     const size_t si = tc_slot(p, bt, h, pos, good);
-    r.ok = good && (WIN ? keys.seen(pos) : pos < keys.end);
+    r.ok = good && pos < L;
     if (!good) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) r.v[u] = make_uint4(0, 0, 0, 0);
@@ -182,7 +169,9 @@ __device__ __forceinline__ void tc_load_v(const PrefillParams &p, const int32_t 
 // 9360 to infinity.  A larger scale is reported as NF_DEVERR_RANGE.
 constexpr uint32_t kTcMaxKScaleBits = 0x6007u;  // 515.5
 constexpr uint32_t kTcMaxVScaleBits = 0x7091u;  // 9352
-// key's dequantised fp16 K row (code x K scale)
+// key's dequantised fp16 K row (code x K scale) into an operand whose blocks of
+// 64 channels are BLK bytes apart
+template <uint32_t BLK = 8192u>
 __device__ __forceinline__ void tc_convert_k(const TcRawK &r, int key, unsigned char *kb) {
     if (r.ok && (r.ks & 0x7FFFu) > kTcMaxKScaleBits) report(NF_DEVERR_RANGE);
     const __half2 sk = u32_h2(r.ok ? (r.ks & 0xFFFFu) * 0x10001u : 0u);
@@ -197,11 +186,12 @@ __device__ __forceinline__ void tc_convert_k(const TcRawK &r, int key, unsigned 
         a.z = h2_u32(__hmul2(u32_h2(a.z), sk)); a.w = h2_u32(__hmul2(u32_h2(a.w), sk));
         c.x = h2_u32(__hmul2(u32_h2(c.x), sk)); c.y = h2_u32(__hmul2(u32_h2(c.y), sk));
         c.z = h2_u32(__hmul2(u32_h2(c.z), sk)); c.w = h2_u32(__hmul2(u32_h2(c.w), sk));
-        *reinterpret_cast<uint4 *>(kb + tc_swz(key, 2 * u, 8192u)) = a;
-        *reinterpret_cast<uint4 *>(kb + tc_swz(key, 2 * u + 1, 8192u)) = c;
+        *reinterpret_cast<uint4 *>(kb + tc_swz(key, 2 * u, BLK)) = a;
+        *reinterpret_cast<uint4 *>(kb + tc_swz(key, 2 * u + 1, BLK)) = c;
     }
 }
 // key's dequantised fp16 V row (code x V scale; 0 past the end)
+template <uint32_t BLK = 8192u>
 __device__ __forceinline__ void tc_convert_v(const TcRawV &r, int key, unsigned char *vb) {
     const uint32_t keep = r.ok ? 0xFFFFFFFFu : 0u;
     if (r.ok) {
@@ -220,7 +210,7 @@ __device__ __forceinline__ void tc_convert_v(const TcRawV &r, int key, unsigned 
         o.y = h2_u32(__hmul2(nib_odd(w), sv));
         o.z = h2_u32(__hmul2(nib_even(w >> 8), sv));
         o.w = h2_u32(__hmul2(nib_odd(w >> 8), sv));
-        *reinterpret_cast<uint4 *>(vb + tc_swz(key, i, 8192u)) = o;
+        *reinterpret_cast<uint4 *>(vb + tc_swz(key, i, BLK)) = o;
     }
 }
 
@@ -239,10 +229,6 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile
     return true;
 }
 
-// WIN: the windowed form (nf_prefill_attn_window).  A CTA's key tiles are those
-// of the sinks and those from its first row's window on; a sequence of length
-// 0 is an unused row of the batch.
-template <bool WIN>
 __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_constant__ PrefillParams p) {
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + TcSmem::kBars);
@@ -303,28 +289,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
     const bool bad_len = L < p.n_q || L > p.max_seqlen;
     const int last_row = min(r0 + kTcRows, p.rows) - 1;
     const int n_keys = bad_len ? 0 : (p.causal ? L - p.n_q + last_row / G + 1 : L);
-    TcKeys keys{0, 0, WIN ? n_keys : L, 0, 0};
-    if (WIN && !bad_len) {
-        keys.n_sink = p.n_sink;
-        keys.lo = max(0, L - p.n_q + r0 / G - p.window + 1);
-        const int first = keys.lo / kTcKeys;
-        if (p.n_sink < keys.lo && (p.n_sink + kTcKeys - 1) / kTcKeys < first) {
-            keys.sinks = (p.n_sink + kTcKeys - 1) / kTcKeys;
-            keys.skip = first - keys.sinks;
-        }
-    }
-    const int T = (n_keys + kTcKeys - 1) / kTcKeys - keys.skip;
+    const int T = (n_keys + kTcKeys - 1) / kTcKeys;
     const int32_t *bt = p.block_table + (size_t)b * p.max_blocks;
 
     if (bad_len) {
-        if (threadIdx.x == 0 && rt == p.row_tiles - 1 && h == 0 && !(WIN && L == 0)) report(NF_DEVERR_SEQLEN);
+        if (threadIdx.x == 0 && rt == p.row_tiles - 1 && h == 0) report(NF_DEVERR_SEQLEN);
         for (int idx = threadIdx.x; idx < kTcRows * kHeadDim; idx += kTcThreads) {
             const int r = r0 + idx / kHeadDim, ch = idx % kHeadDim;
             if (r >= p.rows) continue;
-            if (WIN && p.out_bf16)
-                reinterpret_cast<__nv_bfloat16 *>(p.out)[out_row(r) * kHeadDim + ch] = __float2bfloat16_rn(0.f);
-            else
-                p.out[out_row(r) * kHeadDim + ch] = 0.f;
+            p.out[out_row(r) * kHeadDim + ch] = 0.f;
             if (ch == 0 && p.out_lse) p.out_lse[out_row(r)] = -INFINITY;
         }
     } else if (warp >= 8 && warp < 12 && !*abort_flag) {
@@ -350,10 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
                 for (int e = 0; e < 4; ++e) am = max(am, max((ww[e] << 16) & 0x7FFFFFFFu, ww[e] & 0x7FFF0000u));
             }
             const float amax = __uint_as_float(am);
-            // windowed: a row of subnormals counts as zeros (1 / amax stays finite),
-            // and the row's factor stays positive, so that a hidden key's -inf
-            // times it is -inf
-            const float inv = amax > 0.f && (!WIN || amax >= 1.17549435e-38f) ? 1.0f / amax : 0.f;
+            const float inv = amax > 0.f ? 1.0f / amax : 0.f;
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
                 const uint32_t ww[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
@@ -364,7 +334,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
                 *reinterpret_cast<uint4 *>(smem + TcSmem::kQ + x * 32768 + tc_swz(t, c, 16384u)) =
                     make_uint4(o4[0], o4[1], o4[2], o4[3]);
             }
-            qfs[128 * x + t] = WIN ? fmaxf(amax * p.scale_log2, 1.17549435e-38f) : amax * p.scale_log2;
+            qfs[128 * x + t] = amax * p.scale_log2;
         }
         fence_async_smem();
         mbar_arrive(q_full);
@@ -390,11 +360,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
         };
         if (t < 64) {
             TcRawK ra, rb;
-            ring(ra, rb, [&](int tile, TcRawK &r) { tc_load_k<WIN>(p, bt, keys, h, tile, t, r); },
+            ring(ra, rb, [&](int tile, TcRawK &r) { tc_load_k(p, bt, L, h, tile, t, r); },
                  [&](const TcRawK &r, int key, unsigned char *dst) { tc_convert_k(r, key, dst); }, t, TcSmem::kK);
         } else {
             TcRawV ra, rb;
-            ring(ra, rb, [&](int tile, TcRawV &r) { tc_load_v<WIN>(p, bt, keys, h, tile, t - 64, r); },
+            ring(ra, rb, [&](int tile, TcRawV &r) { tc_load_v(p, bt, L, h, tile, t - 64, r); },
                  [&](const TcRawV &r, int key, unsigned char *dst) { tc_convert_v(r, key, dst); }, t - 64, TcSmem::kV);
         }
     } else if (warp < 8 && !*abort_flag) {
@@ -419,17 +389,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
             tmem_ld32(t_lane + s_col + 64u * sb + 32u, sbv);
             tmem_wait_ld();
 #define SV(i) ((i) < 32 ? sa[(i)] : sbv[(i) - 32])
-            const int key0 = (WIN ? keys.tile(j) : j) * kTcKeys;
+            const int key0 = j * kTcKeys;
             const int nvis = min(kTcKeys, lim - key0 + 1);  // keys of the tile this row sees (may be <= 0)
-            if (WIN) {
-                // hidden: behind the row's position, or before its window and no sink
-                const int first = lim - p.window + 1 - key0, sink = p.n_sink - key0;
-                if (nvis < kTcKeys || (first > 0 && sink < min(first, kTcKeys))) {
-#pragma unroll
-                    for (int i = 0; i < kTcKeys; ++i)
-                        if (i >= nvis || (i < first && i >= sink)) SV(i) = __float_as_uint(-INFINITY);
-                }
-            } else if (nvis < kTcKeys) {
+            if (nvis < kTcKeys) {
 #pragma unroll
                 for (int i = 0; i < kTcKeys; ++i)
                     if (i >= nvis) SV(i) = __float_as_uint(-INFINITY);
@@ -508,7 +470,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
             tc_fence_after();
             const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
             float *dst = row < p.rows ? p.out + out_row(row) * kHeadDim : nullptr;
-            __nv_bfloat16 *dst16 = reinterpret_cast<__nv_bfloat16 *>(p.out) + (row < p.rows ? out_row(row) * kHeadDim : 0);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
@@ -523,15 +484,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
                                                  __uint_as_float(q8[4]) * inv, __uint_as_float(q8[6]) * inv);
                         float4 hi4 = make_float4(__uint_as_float(q8[1]) * inv, __uint_as_float(q8[3]) * inv,
                                                  __uint_as_float(q8[5]) * inv, __uint_as_float(q8[7]) * inv);
-                        if (WIN && p.out_bf16) {
-                            *reinterpret_cast<uint4 *>(dst16 + 32 * c + 8 * g8) =
-                                make_uint4(pack_bf16(lo4.x, lo4.y), pack_bf16(lo4.z, lo4.w), pack_bf16(hi4.x, hi4.y),
-                                           pack_bf16(hi4.z, hi4.w));
-                        } else {
-                            float4 *d4 = reinterpret_cast<float4 *>(dst + 32 * c + 8 * g8);
-                            d4[0] = lo4;
-                            d4[1] = hi4;
-                        }
+                        float4 *d4 = reinterpret_cast<float4 *>(dst + 32 * c + 8 * g8);
+                        d4[0] = lo4;
+                        d4[1] = hi4;
                     }
                 }
             }
