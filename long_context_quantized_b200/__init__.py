@@ -155,9 +155,12 @@ def _dptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream):
     if stream is None:  # the current stream's handle, without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -382,23 +385,44 @@ def _refuse(where, message):
     raise NfError(NF_ERR_INVALID_ARG, where, message)
 
 
-# The checks below run at every call, a few hundred nanoseconds each: a call's
-# host time is most of what a short kernel costs its caller.
+# The checks below run at every call: a call's host time is most of what a
+# short kernel costs its caller, so the good case is a few comparisons and what
+# was wrong is worked out only then.
+_i32 = torch.int32
+
+
+def _bad(where, name, t, dtype, device):
+    _refuse(where, f"{name}: {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}; "
+                   f"expected a contiguous {dtype} tensor on cuda:{device}")
+
+
 def _current(where, t) -> int:
     """The device number of t, which must be the current CUDA device."""
     d = t.get_device()
     if d < 0:
         _refuse(where, "tensors must be on a CUDA device")
-    if d != torch.cuda.current_device():
-        _refuse(where, f"tensors are on cuda:{d}, the current device is cuda:{torch.cuda.current_device()}")
+    if d != _current_device():
+        _refuse(where, f"tensors are on cuda:{d}, the current device is cuda:{_current_device()}")
     return d
 
 
 def _on(where, name, t, device: int, dtype):
     """t must be contiguous, of dtype, on the device."""
     if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
-        _refuse(where, f"{name}: {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}; "
-                       f"expected a contiguous {dtype} tensor on cuda:{device}")
+        _bad(where, name, t, dtype, device)
+
+
+def _vector(where, name, t, device: int, n: int) -> int:
+    """The address of t, which must be contiguous int32 [n] on the device."""
+    if t.dtype is not _i32 or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
+        if t.dim() != 1 or len(t) != n:
+            _refuse(where, f"{name}: {tuple(t.shape)}, expected [{n}]")
+        _bad(where, name, t, _i32, device)
+    return t.data_ptr()
+
+
+def _call_stream(stream, device: int):
+    return _raw_stream(device) if stream is None else _stream(stream)
 
 
 def nf_decode_attn_window_workspace_size(batch, n_q, num_q_heads, num_kv_heads, max_seqlen, num_sms=None):
@@ -409,25 +433,27 @@ def nf_decode_attn_window_workspace_size(batch, n_q, num_q_heads, num_kv_heads, 
 
 
 def _window_args(where, kv, q, block_table, seqlens, out, out_lse):
-    """Checks what both windowed calls take; returns q's shape and device."""
+    """Checks what both windowed calls take; returns q's shape, the device and addresses."""
     d = _current(where, q)
     shape = q.shape
     if len(shape) != 4 or shape[3] != HEAD_DIM or not q.is_contiguous():
         _refuse(where, "q must be contiguous [batch][n_q][H_q][128]")
-    _on(where, "block_table", block_table, d, torch.int32)
-    _on(where, "seqlens", seqlens, d, torch.int32)
-    _on(where, "out", out, d, out.dtype)
+    B = shape[0]
+    if block_table.dtype is not _i32 or block_table.get_device() != d or not block_table.is_contiguous():
+        _bad(where, "block_table", block_table, _i32, d)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        _refuse(where, "block_table must be [batch][max_blocks] with q's batch")
+    if out.get_device() != d or out.shape != shape or not out.is_contiguous():
+        _refuse(where, f"out must be contiguous, of q's shape, on cuda:{d}")
     if kv.device != d:
         _refuse(where, f"the pool is on cuda:{kv.device}, q on cuda:{d}")
-    if out.shape != shape:
-        _refuse(where, "out must have q's shape")
+    lse = None
     if out_lse is not None:
         _on(where, "out_lse", out_lse, d, torch.float32)
         if out_lse.shape != shape[:3]:
             _refuse(where, "out_lse must be [batch][n_q][H_q]")
-    if block_table.dim() != 2 or len(block_table) != shape[0] or seqlens.dim() != 1 or len(seqlens) != shape[0]:
-        _refuse(where, "block_table [batch][max_blocks] and seqlens [batch] must have q's batch")
-    return shape, d
+        lse = out_lse.data_ptr()
+    return shape, d, _vector(where, "seqlens", seqlens, d, B), lse
 
 
 def nf_decode_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int, window: int, n_sink: int,
@@ -436,28 +462,30 @@ def nf_decode_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int,
     sees the keys t <= P with t > P - window or t < n_sink (see nf.h).  out
     (fp32 or bf16) has the shape of q [batch][n_q][H_q][128]; seqlens 0 marks an
     unused row of the batch."""
-    (B, n_q, H_q, _), d = _window_args("nf_decode_attn_window", kv, q, block_table, seqlens, out, out_lse)
+    (B, n_q, H_q, _), d, lens, lse = _window_args("nf_decode_attn_window", kv, q, block_table, seqlens, out, out_lse)
     if workspace is None:
         raise NfError(NF_ERR_WORKSPACE, "nf_decode_attn_window", "workspace tensor required "
                       "(size: nf_decode_attn_window_workspace_size)")
-    _on("nf_decode_attn_window", "workspace", workspace, d, workspace.dtype)
-    st = load_library().nf_decode_attn_window(
-        kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1],
-        seqlens.data_ptr(), max_seqlen, window, n_sink, softmax_scale, out.data_ptr(), _dtype_code(out.dtype),
-        None if out_lse is None else out_lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
-    _check(st, "nf_decode_attn_window")
+    if workspace.get_device() != d or not workspace.is_contiguous():
+        _bad("nf_decode_attn_window", "workspace", workspace, workspace.dtype, d)
+    st = (_lib or load_library()).nf_decode_attn_window(
+        kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1], lens,
+        max_seqlen, window, n_sink, softmax_scale, out.data_ptr(), _dtype_code(out.dtype), lse, workspace.data_ptr(),
+        workspace.nbytes, _call_stream(stream, d))
+    if st:
+        _check(st, "nf_decode_attn_window")
 
 
 def nf_prefill_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int, window: int, n_sink: int,
                            softmax_scale: float, out, out_lse=None, stream=None):
     """Chunked-prefill attention with a sliding window and sinks (see nf.h and
     nf_decode_attn_window): bf16 q over a K8/V4 pool, out fp32 or bf16."""
-    (B, n_q, H_q, _), d = _window_args("nf_prefill_attn_window", kv, q, block_table, seqlens, out, out_lse)
-    st = load_library().nf_prefill_attn_window(
-        kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1],
-        seqlens.data_ptr(), max_seqlen, window, n_sink, softmax_scale, out.data_ptr(), _dtype_code(out.dtype),
-        None if out_lse is None else out_lse.data_ptr(), _stream(stream))
-    _check(st, "nf_prefill_attn_window")
+    (B, n_q, H_q, _), d, lens, lse = _window_args("nf_prefill_attn_window", kv, q, block_table, seqlens, out, out_lse)
+    st = (_lib or load_library()).nf_prefill_attn_window(
+        kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1], lens,
+        max_seqlen, window, n_sink, softmax_scale, out.data_ptr(), _dtype_code(out.dtype), lse, _call_stream(stream, d))
+    if st:
+        _check(st, "nf_prefill_attn_window")
 
 
 class Rope:
@@ -477,12 +505,12 @@ class Rope:
         self.ref = ctypes.byref(self.c)
 
 
-def _heads(where, name, t, dtype, device, batch, n_new, heads):
-    if t.shape != (batch, n_new, heads, HEAD_DIM) or t.dtype is not dtype or t.get_device() != device:
-        _refuse(where, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} "
-                       f"{(batch, n_new, heads, HEAD_DIM)} on cuda:{device}")
+def _heads(where, name, t, dtype, device, shape):
+    """The rows of t [batch][n_new][heads][128], whose heads must be contiguous."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        _refuse(where, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape} on cuda:{device}")
     sb, st, sh, sc = t.stride()
-    if (sc != 1 or (sh != HEAD_DIM and heads > 1)) and t.numel():
+    if (sc != 1 or (sh != HEAD_DIM and shape[2] > 1)) and t.numel():
         _refuse(where, f"{name}: the heads of a token must be contiguous")
     return nf_heads(t.data_ptr(), sb, st)
 
@@ -499,39 +527,34 @@ def nf_rope_append_quant(kv: KVLayer, rope: Rope, positions, q, k_new, v_new, bl
     d = _current(where, k_new)
     if k_new.dim() != 4:
         _refuse(where, "k_new must be [batch][n_new][H_kv][128]")
-    B, n_new = k_new.shape[0], k_new.shape[1]
+    B, n_new = k_new.shape[:2]
     dtype = k_new.dtype
-    k = _heads(where, "k_new", k_new, dtype, d, B, n_new, kv.num_kv_heads)
-    v = _heads(where, "v_new", v_new, dtype, d, B, n_new, kv.num_kv_heads)
+    shape = (B, n_new, kv.num_kv_heads, HEAD_DIM)
+    k = _heads(where, "k_new", k_new, dtype, d, shape)
+    v = _heads(where, "v_new", v_new, dtype, d, shape)
     if q is not None:
         H_q = q.shape[2] if q.dim() == 4 else 0
-        qh = _heads(where, "q", q, dtype, d, B, n_new, H_q)
+        qh = _heads(where, "q", q, dtype, d, (B, n_new, H_q, HEAD_DIM))
         if q_out is None or q_out.shape != q.shape:
             _refuse(where, "q_out must have q's shape")
         _on(where, "q_out", q_out, d, dtype)
         out = q_out.data_ptr()
     else:
         H_q, qh, out = 0, nf_heads(None, 0, 0), None
-    _on(where, "positions", positions, d, torch.int32)
-    _on(where, "block_table", block_table, d, torch.int32)
-    _on(where, "seqlens_before", seqlens_before, d, torch.int32)
+    _on(where, "positions", positions, d, _i32)
+    _on(where, "block_table", block_table, d, _i32)
     if kv.device != d or rope.device != d:
         _refuse(where, "the pool, inv_freq and the inputs must be on one device")
     if positions.shape != (B, n_new, rope.n_axes):
         _refuse(where, f"positions must be [batch][n_new][{rope.n_axes}]")
-    if block_table.dim() != 2 or len(block_table) != B or seqlens_before.shape != (B,):
-        _refuse(where, "block_table and seqlens_before must have the inputs' batch")
-    valid = None
-    if n_valid is not None:
-        _on(where, "n_valid", n_valid, d, torch.int32)
-        if n_valid.shape != (B,):
-            _refuse(where, "n_valid must be [batch]")
-        valid = n_valid.data_ptr()
-    st = load_library().nf_rope_append_quant(
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        _refuse(where, "block_table must be [batch][max_blocks] with the inputs' batch")
+    st = (_lib or load_library()).nf_rope_append_quant(
         kv.ref, rope.ref, positions.data_ptr(), ctypes.byref(qh), ctypes.byref(k), ctypes.byref(v), _dtype_code(dtype),
-        B, n_new, H_q, block_table.data_ptr(), block_table.shape[1], seqlens_before.data_ptr(), valid, out,
-        _stream(stream))
-    _check(st, where)
+        B, n_new, H_q, block_table.data_ptr(), block_table.shape[1], _vector(where, "seqlens_before", seqlens_before, d, B),
+        None if n_valid is None else _vector(where, "n_valid", n_valid, d, B), out, _call_stream(stream, d))
+    if st:
+        _check(st, where)
 
 
 class KVLayers:
@@ -553,8 +576,8 @@ class KVLayers:
 
 def _pages_args(where, refs, block_table) -> int:
     d = _current(where, refs)
-    _on(where, "refs", refs, d, torch.int32)
-    _on(where, "block_table", block_table, d, torch.int32)
+    _on(where, "refs", refs, d, _i32)
+    _on(where, "block_table", block_table, d, _i32)
     if refs.dim() != 1 or block_table.dim() != 2:
         _refuse(where, "refs must be [num_blocks], block_table [rows][max_blocks]")
     return d
@@ -562,36 +585,32 @@ def _pages_args(where, refs, block_table) -> int:
 
 def _pool_args(where, layers, refs, block_table, workspace) -> int:
     d = _pages_args(where, refs, block_table)
-    if len(refs) != layers.num_blocks or layers.device != d:
+    if refs.shape[0] != layers.num_blocks or layers.device != d:
         _refuse(where, "refs must have one count per block of the pool, on its device")
     _on(where, "workspace", workspace, d, workspace.dtype)
     return d
 
 
-def _rows(where, name, t, d, n):
-    _on(where, name, t, d, torch.int32)
-    if t.dim() != 1 or len(t) != n:
-        _refuse(where, f"{name}: {tuple(t.shape)}, expected [{n}]")
-    return t.data_ptr()
-
-
 def _range_call(where, call, refs, block_table, from_pos, to_pos, stream):
     d = _pages_args(where, refs, block_table)
     rows, width = block_table.shape
-    _check(call(refs.data_ptr(), len(refs), block_table.data_ptr(), rows, width, _rows(where, "from_pos", from_pos, d, rows),
-                _rows(where, "to_pos", to_pos, d, rows), _stream(stream)), where)
+    st = call(refs.data_ptr(), refs.shape[0], block_table.data_ptr(), rows, width,
+              _vector(where, "from_pos", from_pos, d, rows), _vector(where, "to_pos", to_pos, d, rows),
+              _call_stream(stream, d))
+    if st:
+        _check(st, where)
 
 
 def nf_kv_reserve(refs, block_table, from_pos, to_pos, stream=None):
     """Fresh pages for the positions [from_pos[b], to_pos[b]) of every table
     row that have none (see nf.h): the lowest free blocks, in row order."""
-    _range_call("nf_kv_reserve", load_library().nf_kv_reserve, refs, block_table, from_pos, to_pos, stream)
+    _range_call("nf_kv_reserve", (_lib or load_library()).nf_kv_reserve, refs, block_table, from_pos, to_pos, stream)
 
 
 def nf_kv_release(refs, block_table, from_pos, to_pos, stream=None):
     """Give up the pages wholly inside [from_pos[b], to_pos[b]) of every table
     row (see nf.h): behind a window, or a whole sequence."""
-    _range_call("nf_kv_release", load_library().nf_kv_release, refs, block_table, from_pos, to_pos, stream)
+    _range_call("nf_kv_release", (_lib or load_library()).nf_kv_release, refs, block_table, from_pos, to_pos, stream)
 
 
 def nf_kv_copy_blocks(layers: KVLayers, src, dst, stream=None):
@@ -601,9 +620,10 @@ def nf_kv_copy_blocks(layers: KVLayers, src, dst, stream=None):
     if layers.device != d:
         _refuse(where, f"the pool is on cuda:{layers.device}, src on cuda:{d}")
     n = len(src) if src.dim() == 1 else -1
-    st = load_library().nf_kv_copy_blocks(layers.c, len(layers), _rows(where, "src", src, d, n), _rows(where, "dst", dst, d, n),
-                                          n, _stream(stream))
-    _check(st, where)
+    st = (_lib or load_library()).nf_kv_copy_blocks(layers.c, len(layers), _vector(where, "src", src, d, n), _vector(where, "dst", dst, d, n),
+                                          n, _call_stream(stream, d))
+    if st:
+        _check(st, where)
 
 
 def nf_kv_pages_workspace_size(num_blocks: int, n_forks: int = 0) -> int:
@@ -619,19 +639,21 @@ def nf_kv_fork(layers: KVLayers, refs, block_table, src_rows, dst_rows, seqlens,
     d = _pool_args(where, layers, refs, block_table, workspace)
     rows, width = block_table.shape
     n = len(src_rows) if src_rows.dim() == 1 else -1
-    st = load_library().nf_kv_fork(
+    st = (_lib or load_library()).nf_kv_fork(
         layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), rows, width,
-        _rows(where, "src_rows", src_rows, d, n), _rows(where, "dst_rows", dst_rows, d, n), n,
-        _rows(where, "seqlens", seqlens, d, rows), workspace.data_ptr(), workspace.nbytes, _stream(stream))
-    _check(st, where)
+        _vector(where, "src_rows", src_rows, d, n), _vector(where, "dst_rows", dst_rows, d, n), n,
+        _vector(where, "seqlens", seqlens, d, rows), workspace.data_ptr(), workspace.nbytes, _call_stream(stream, d))
+    if st:
+        _check(st, where)
 
 
 def nf_kv_compact(layers: KVLayers, refs, block_table, workspace, stream=None):
     """Move the blocks in use to the front of the pool, in every layer, and
     renumber the table (see nf.h)."""
     where = "nf_kv_compact"
-    _pool_args(where, layers, refs, block_table, workspace)
+    d = _pool_args(where, layers, refs, block_table, workspace)
     rows, width = block_table.shape
-    st = load_library().nf_kv_compact(layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), rows, width,
-                                      workspace.data_ptr(), workspace.nbytes, _stream(stream))
-    _check(st, where)
+    st = (_lib or load_library()).nf_kv_compact(layers.c, len(layers), refs.data_ptr(), block_table.data_ptr(), rows, width,
+                                      workspace.data_ptr(), workspace.nbytes, _call_stream(stream, d))
+    if st:
+        _check(st, where)

@@ -59,16 +59,20 @@ __device__ __forceinline__ __half make_scale(float a, float q, float &sigma) {
 }
 
 // Codes of four channels: round_half_even(fp32(x / sigma)) clamped to [-q, q], 0
-// when sigma is 0.  The IEEE quotient is only worked out where it matters: t =
-// x * rcp(sigma) is within 2^-22 of x / sigma relatively and the fp32 quotient
-// within 2^-24, so for |t| <= 128 both lie within 2^-14 of each other, and where
-// t is further than 2^-13 from every border n + 1/2 the two round alike (beyond
-// 128 both are clamped).  About one warp in 30 has a lane that is closer and
-// divides.
+// when sigma is 0.
+// QUICK: the IEEE quotient is only worked out where it matters.  t = x *
+// rcp(sigma) is within 2^-22 of x / sigma relatively and the fp32 quotient within
+// 2^-24, so for |t| <= 128 both lie within 2^-14 of each other, and where t is
+// further than 2^-13 from every border n + 1/2 the two round alike (beyond 128
+// both are clamped).  About one warp in 30 has a lane that is closer and divides.
+// This pays where many rows are bound by instructions (8192 tokens x 8 heads
+// appended: 23.8 instead of 26.2 us); for the few rows of a decode step, which
+// wait on latency, the second path costs 1 us and the divisions are faster.
+template <bool QUICK>
 __device__ __forceinline__ void make_codes(const float (&x)[4], float sigma, int q, int (&code)[4]) {
     const float r = sigma == 0.0f ? 0.0f : rcp_approx(sigma);  // sigma >= 2^-24: normal
     float t[4];
-    bool sure = true;
+    bool sure = QUICK;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         t[c] = x[c] * r;
@@ -83,9 +87,10 @@ __device__ __forceinline__ void make_codes(const float (&x)[4], float sigma, int
 }
 
 // Four int8 codes (absmax / 127 scale) in one word.
+template <bool QUICK>
 __device__ __forceinline__ uint32_t pack_codes8(const float (&x)[4], float sigma) {
     int code[4];
-    make_codes(x, sigma, 127, code);
+    make_codes<QUICK>(x, sigma, 127, code);
     return prmt(prmt((uint32_t)code[0], (uint32_t)code[1], 0x0040), prmt((uint32_t)code[2], (uint32_t)code[3], 0x0040),
                 0x5410);
 }
@@ -103,11 +108,12 @@ __device__ __forceinline__ void quant_row8(const float (&x)[4], int lane, int8_t
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     float sigma;
     const __half h = make_scale(a, 127.0f, sigma);
-    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = pack_codes8(x, sigma);
+    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = pack_codes8<false>(x, sigma);
     if (lane == 0) *scale = h;
 }
 
 // Four e4m3 codes (absmax / 448 scale) in one word.
+template <bool QUICK>
 __device__ __forceinline__ uint32_t pack_codes_f8(const float (&x)[4], float sigma) {
     // as make_codes: t is within 2^-22 of the fp32 quotient relatively (about 2
     // fp32 steps); an e4m3 border of a normal result lies where the 20 fp32
@@ -115,7 +121,7 @@ __device__ __forceinline__ uint32_t pack_codes_f8(const float (&x)[4], float sig
     // and above the subnormal results, both round alike
     const float r = sigma == 0.0f ? 0.0f : rcp_approx(sigma);
     float t[4];
-    bool sure = true;
+    bool sure = QUICK;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         t[c] = x[c] * r;
@@ -137,7 +143,7 @@ __device__ __forceinline__ void quant_row_f8(const float (&x)[4], int lane, uint
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     float sigma;
     const __half h = make_scale(a, 448.0f, sigma);
-    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = pack_codes_f8(x, sigma);
+    *reinterpret_cast<uint32_t *>(codes + 4 * lane) = pack_codes_f8<false>(x, sigma);
     if (lane == 0) *scale = h;
 }
 
@@ -218,7 +224,7 @@ __device__ __forceinline__ void store_v_row(const AppendParams &p, const float (
     float sv;
     const __half hv = make_scale(av, 7.0f, sv);
     int code[4];
-    make_codes(v, sv, 7, code);
+    make_codes<false>(v, sv, 7, code);
     *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(p.v_codes) + si * (kHeadDim / 2) + 2 * lane) =
         (uint16_t)pack_codes4(code);
     if ((lane & 7) == 0) p.v_scales[si * (kHeadDim / kVGroup) + (lane >> 3)] = hv;

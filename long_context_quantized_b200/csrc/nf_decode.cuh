@@ -65,6 +65,8 @@
 // and the kernel runs to its end without further waits.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda.h>  // CUtensorMap (a plain struct; no driver call is made here)
 
 #include "nf_common.cuh"
@@ -281,7 +283,17 @@ struct PieceWalker {
     long long s0, xs, xe;      // position of the segment's first chunk, piece [xs, xe)
     __device__ bool next() {
         while (x < end) {
-            while (b + 1 <= batch && base[b + 1] <= x) ++b;
+            if (base[b + 1] <= x) {
+                // the sequence that holds position x (x < end <= base[batch])
+                int lo = b + 1, hi = batch - 1;
+                if (base[lo + 1] > x) hi = lo;
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (base[mid + 1] > x) hi = mid;
+                    else lo = mid + 1;
+                }
+                b = lo;
+            }
             const long long span = pad + (long long)C[b];
             pb = b;
             ph = (int)((x - base[b]) / span);
@@ -308,6 +320,36 @@ __device__ __forceinline__ int stage_end(int cx, int cx_end) {
 
 __device__ __forceinline__ int owner_cta(long long x, long long W, int P) {
     return (int)(((x + 1) * P - 1) / W);
+}
+
+// The work cut's tables (one warp): the sequences' lengths (0: no valid keys),
+// chunks, and by a prefix sum over the batch their segments' positions.
+template <bool WIN>
+__device__ __forceinline__ void cut_plan(const DecodeParams &p, int pad, int lane, int *seqC, int *seqL,
+                                         long long *seqBase) {
+    long long acc = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int C = 0;
+        if (b < p.batch) {
+            const int L = p.seqlens[b];
+            const bool ok = L >= p.n_q && L <= p.max_seqlen;
+            if (!ok && blockIdx.x == 0 && !(WIN && L == 0)) report(NF_DEVERR_SEQLEN);
+            if (ok) C = (L + kChunk - 1) / kChunk - (WIN ? win_span(L, p.n_q, p.window, p.n_sink).skip : 0);
+            seqC[b] = C;
+            seqL[b] = ok ? L : 0;
+        }
+        const long long len = C ? (long long)(C + pad) * p.num_kv_heads : 0;
+        long long inc = len;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        if (b < p.batch) seqBase[b] = acc + inc - len;
+        acc += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) seqBase[p.batch] = acc;
 }
 
 // Brings the query rows of (sequence b, kv-head h) into L2 -- thread t < rows
@@ -1069,24 +1111,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
     // workspace are touched.
     if (!p.early_kv) pdl_wait();
     pdl_trigger();
-    if (warp == 0) {
-        for (int b = lane; b < p.batch; b += 32) {
-            const int L = p.seqlens[b];
-            const bool ok = L >= p.n_q && L <= p.max_seqlen;
-            if (!ok && blockIdx.x == 0 && !(WIN && L == 0)) report(NF_DEVERR_SEQLEN);
-            seqC[b] = ok ? (L + kChunk - 1) / kChunk - (WIN ? win_span(L, p.n_q, p.window, p.n_sink).skip : 0) : 0;
-            seqL[b] = ok ? L : 0;
-        }
-        __syncwarp();
-        if (lane == 0) {
-            long long acc = 0;
-            for (int b = 0; b < p.batch; ++b) {
-                seqBase[b] = acc;
-                acc += seqC[b] ? (long long)(seqC[b] + kSegPad) * H : 0;
-            }
-            seqBase[p.batch] = acc;
-        }
-    }
+    if (warp == 0) cut_plan<WIN>(p, kSegPad, lane, seqC, seqL, seqBase);
     __syncthreads();
     const long long W = seqBase[p.batch];
     // CTAs taking part: never more than there are chunks, so that every CTA
@@ -1218,7 +1243,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         }
     }
 
-    const int CW = kConsumerWarps / p.n_rg;  // warps per row group
+    const int CW = NT == 1 ? kConsumerWarps : kConsumerWarps / p.n_rg;  // warps per row group
     const int rg = warp / CW, slot = warp % CW;
     const int g = lane >> 2, t = lane & 3;
     const int row0 = rg * NR;
@@ -1253,12 +1278,31 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         lo.ks = lo.vs = 0;
     }
 
+    // scaled caches with at most 8 rows: warp r encodes row r of a piece, and has it
+    // loaded while it works on the piece before
+    constexpr bool QAHEAD = K8 && NT == 1;
+    typename std::conditional<QF32, float4, uint2>::type q_raw{};
+    auto load_q = [&](int b, int h) {
+        if (warp < p.rows) {
+            const int j = warp / p.group, gq = warp % p.group;
+            const size_t qoff = (((size_t)b * p.n_q + j) * p.num_q_heads + (size_t)h * p.group + gq) * kHeadDim + 4 * lane;
+            if constexpr (QF32) q_raw = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + qoff);
+            else q_raw = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + qoff);
+        }
+    };
+    bool piece = walk.next();
+    if (QAHEAD && piece) load_q(walk.pb, walk.ph);
+
     int stage = 0;
     uint32_t phase = 0;      // parity of the ring's current round
     uint32_t fin_phase = 0;  // parity of the final merge's copy barrier
-    while (walk.next()) {
+    while (piece) {
         const int b = walk.pb, h = walk.ph;
         const int L = seqL[b];  // (read once at the start; 0 for a sequence with no valid key)
+        // the next piece (its stages may be in the ring when this one ends); with 16
+        // rows a warp holds too many registers to carry it through the keys
+        PieceWalker nx = walk;
+        bool more = nx.next();
         // query fragments of this (sequence, kv-head): lane (g, t) holds row g of
         // tile nt, channels 32t..32t+31 (int8 K: k-step ks takes channels 32t + 8ks
         // + 0..3 and + 4..7; fp8 K: 32t + 4ks + 0..3) or 32u + 8t + 4h + 0..3
@@ -1273,16 +1317,21 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
             // e=2,3] (an f16 A fragment: rows g hold hi, rows g + 8 lo).
             uint32_t *qsm = reinterpret_cast<uint32_t *>(sm_o);
             float *qwsm = reinterpret_cast<float *>(sm_o) + kMaxRows * (F8 ? 128 : 64);
-            for (int r = warp; r < p.rows; r += kConsumerWarps) {
+            auto q_at = [&](int r) {
                 const int j = r / p.group, gq = r % p.group;
-                const size_t qoff =
-                    (((size_t)b * p.n_q + j) * p.num_q_heads + (size_t)h * p.group + gq) * kHeadDim + 4 * lane;
+                return (((size_t)b * p.n_q + j) * p.num_q_heads + (size_t)h * p.group + gq) * kHeadDim + 4 * lane;
+            };
+            for (int r = warp; r < p.rows; r += kConsumerWarps) {
                 float x[4];
-                if (QF32) {
-                    const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + qoff);
+                if constexpr (QF32) {
+                    float4 v;
+                    if constexpr (QAHEAD) v = q_raw;
+                    else v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + q_at(r));
                     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
                 } else {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + qoff);
+                    uint2 v;
+                    if constexpr (QAHEAD) v = q_raw;
+                    else v = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + q_at(r));
                     x[0] = __uint_as_float(v.x << 16);
                     x[1] = __uint_as_float(v.x & 0xFFFF0000u);
                     x[2] = __uint_as_float(v.y << 16);
@@ -1342,10 +1391,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
                 if (lane == 0) qwsm[r] = s1 / 254.0f * p.scale_log2;
             }
             named_sync(1, kConsumerWarps * 32);
-            {
-                // the next piece's query rows into L2, ahead of its start
-                PieceWalker nx = walk;
-                if (nx.next()) prefetch_q_rows<QF32>(p, nx.pb, nx.ph, threadIdx.x);
+            // the next piece's query rows into registers (or L2), ahead of its start
+            if (more) {
+                if (QAHEAD) load_q(nx.pb, nx.ph);
+                else prefetch_q_rows<QF32>(p, nx.pb, nx.ph, threadIdx.x);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -1430,6 +1479,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         }
 
         // ---- merge the consumer warps of each row group (shared memory)
+        if (NT != 1) {
+            nx = walk;
+            more = nx.next();
+        }
         const int s_id = b * H + h;
         const int first = owner_cta(walk.s0, W, P);
         const int last = owner_cta(walk.s0 + seqC[b] - 1, W, P);
@@ -1500,11 +1553,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
             }
         }
         named_sync(1, kConsumerWarps * 32);
-        PieceWalker rest = walk;
-        const bool more = rest.next();  // another piece follows: its stages may be in the ring
         finish_piece_single<kConsumerWarps * 32, 1, WIN>(p, s_id, first, n_pieces, rows_here, b, h, !more, smem,
                                                     NS * ST::kStride, fin_bar, fin_phase, sm_o, SM::kMergeFloats,
                                                     misc);
+        walk = nx;
+        piece = more;
     }
 }
 

@@ -391,12 +391,15 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
     }
     if (!p.early_kv) pdl_wait();
     pdl_trigger();
-    if (warp == 0) {
+    if (WIN) {
+        if (warp == 0) cut_plan<true>(p, kDtSegPad, lane, seqC, seqL, seqBase);
+    } else if (warp == 0) {
+        // (one long sequence as a rule: the prefix sum over lanes of cut_plan costs it 0.5 us)
         for (int b = lane; b < p.batch; b += 32) {
             const int L = p.seqlens[b];
             const bool ok = L >= p.n_q && L <= p.max_seqlen;
-            if (!ok && blockIdx.x == 0 && !(WIN && L == 0)) report(NF_DEVERR_SEQLEN);
-            seqC[b] = ok ? (L + kChunk - 1) / kChunk - (WIN ? win_span(L, p.n_q, p.window, p.n_sink).skip : 0) : 0;
+            if (!ok && blockIdx.x == 0) report(NF_DEVERR_SEQLEN);
+            seqC[b] = ok ? (L + kChunk - 1) / kChunk : 0;
             seqL[b] = ok ? L : 0;
         }
         __syncwarp();

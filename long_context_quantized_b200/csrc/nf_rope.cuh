@@ -124,8 +124,8 @@ __device__ __forceinline__ void store_row16(const float (&x)[4], const float (&y
     }
     float sigma;
     const __half h = make_scale(group_absmax<16>(x, y), FMT == NF_KV_F8 ? 448.0f : 127.0f, sigma);
-    const uint32_t w0 = FMT == NF_KV_F8 ? pack_codes_f8(x, sigma) : pack_codes8(x, sigma);
-    const uint32_t w1 = FMT == NF_KV_F8 ? pack_codes_f8(y, sigma) : pack_codes8(y, sigma);
+    const uint32_t w0 = FMT == NF_KV_F8 ? pack_codes_f8<true>(x, sigma) : pack_codes8<true>(x, sigma);
+    const uint32_t w1 = FMT == NF_KV_F8 ? pack_codes_f8<true>(y, sigma) : pack_codes8<true>(y, sigma);
     if (store) {
         uint8_t *row = static_cast<uint8_t *>(codes) + si * kHeadDim;
         *reinterpret_cast<uint32_t *>(row + c0) = w0;
@@ -142,8 +142,8 @@ __device__ __forceinline__ void store_v16(const AppendParams &a, const float (&x
         float sigma;
         const __half h = make_scale(group_absmax<4>(x, y), 7.0f, sigma);
         int lo[4], hi[4];
-        make_codes(x, sigma, 7, lo);
-        make_codes(y, sigma, 7, hi);
+        make_codes<true>(x, sigma, 7, lo);
+        make_codes<true>(y, sigma, 7, hi);
         if (store) {
             reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.v_codes) + si * (kHeadDim / 2))[m] =
                 pack_codes4(lo) | (pack_codes4(hi) << 16);
