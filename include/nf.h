@@ -384,8 +384,8 @@ nf_status nf_prefill_attn(const nf_kv_layer *kv, const void *q, int32_t q_dtype,
  *     read only where they share a 32-key chunk with seen ones, and take no
  *     part in the result, whatever they are.
  *   softmax_scale > 0; max_seqlen <= 2^30.
- *   All formats and row counts run on the mma.sync kernel (up to 64 rows per
- *     kv-head, group * n_q).
+ *   Up to 64 rows per kv-head (group * n_q); 9 to 32 of them over K8/V4, K8V8 and
+ *     fp8 pools run on tcgen05, as nf_decode_attn's do.
  * workspace: at least nf_decode_attn_window_workspace_size(...) bytes, 256-byte
  *   aligned, zero-filled before its first use; left as nf_decode_attn leaves
  *   its own, and interchangeable with it.
@@ -402,9 +402,14 @@ nf_status nf_decode_attn_window(const nf_kv_layer *kv, const void *q, int32_t q_
 /*
  * nf_prefill_attn_window -- nf_prefill_attn with a sliding window and sinks:
  * the same visibility for the n_q queries of a prompt chunk (or of a whole
- * prompt, n_q = seqlens[b]).  K8/V4 pool and bf16 q as for nf_prefill_attn;
- * out of out_dtype, unused rows of length 0, released pages and softmax_scale
- * > 0 as for nf_decode_attn_window.
+ * prompt, n_q = seqlens[b]).  K8/V4 pool, bf16 q and the range of K and V as for
+ * nf_prefill_attn (NF_DEVERR_RANGE; only keys that some query sees are looked
+ * at); out of out_dtype, unused rows of length 0, released pages and
+ * softmax_scale > 0 as for nf_decode_attn_window.  At most 2^20 q-heads per
+ * kv-head.
+ * Numerics: each query row is scaled by a power of two to max |q| in [1, 2) and
+ *   held in fp16; K and V as in nf_prefill_attn; scores, softmax statistics,
+ *   weights and row sums in fp32, the weights rounded to fp16 for P . V.
  */
 nf_status nf_prefill_attn_window(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int32_t batch,
                                  int32_t n_q, int32_t num_q_heads, const int32_t *block_table,
@@ -438,7 +443,7 @@ nf_status nf_prefill_attn_window(const nf_kv_layer *kv, const void *q, int32_t q
  *   memory when q is contiguous.  num_q_heads may be 0 (q and q_out unused).
  * n_valid: int32 [batch] (device) or NULL: tokens t >= n_valid[b] are padding;
  *   nothing of them is read, turned or written.
- * Numerics: angles are exact to about 2^-50 of a turn at any position.  Queries
+ * Numerics: angles are exact to about 2^-52 of a turn at any position.  Queries
  *   are turned in fp32 and rounded once; keys are turned in fp64, rounded to
  *   fp32 once and then quantised by the pool format's rule (see nf_kv_layer),
  *   so the pool's bytes are those of this definition.

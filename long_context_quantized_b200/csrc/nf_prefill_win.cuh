@@ -57,8 +57,9 @@ struct PwSmem {
     static constexpr int kV = kK + kPwStages * 16384;       // [stages][16384]
     static constexpr int kBars = kV + kPwStages * 16384;
     static constexpr int kQf = kBars + 256;    // float [256]: the rows' factors
-    static constexpr int kRed = kQf + 1024;    // float [2 halves][256]: the halves' row maxima, then sums
-    static constexpr int kMisc = kRed + 2048;  // tensor memory address, abort flag
+    static constexpr int kRed = kQf + 1024;    // float [2][2 halves][256]: the halves' row maxima; their sums
+    static constexpr int kLeave = kRed + 4096; // int [16]: a softmax warp's wait gave up
+    static constexpr int kMisc = kLeave + 64;  // tensor memory address, abort flag
     static constexpr int kBytes = kMisc + 16;
     static_assert(kBytes <= 232448, "shared memory per CTA");
 };
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
         mbar_init(o_full, 2);
         mbar_init(drain, 4);
         *abort_flag = 0;
+        for (int i = 0; i < 16; ++i) reinterpret_cast<volatile int *>(smem + PwSmem::kLeave)[i] = 0;
         // the swizzled operands need 1024-byte alignment of the window
         if (smem_addr(smem) & 1023u) {
             if (blockIdx.x == 0 && h == 0 && b == 0) report(NF_DEVERR_INTERNAL);
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
         const int x = warp >> 3, hf = (warp >> 2) & 1, r = threadIdx.x & 127;
         const uint32_t pair_bar = 1 + 4 * x + (warp & 3);  // the two warps of these rows
         float *red_row = red + 128 * x + r;                // + 256: the other half's
+        volatile int *leave = reinterpret_cast<volatile int *>(smem + PwSmem::kLeave);
         const int row = r0 + 128 * x + r;
         const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         // this half's scores and weights, and its half of O's columns
@@ -264,8 +267,8 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
                 for (int e = 0; e < 4; ++e) am = max(am, max((ww[e] << 16) & 0x7FFFFFFFu, ww[e] & 0x7FFF0000u));
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-                const uint32_t ex = am >> 23;
-                const float up = __uint_as_float((254u - min(ex, 253u)) << 23);
+                const uint32_t ex = min(max(am >> 23, 1u), 253u);
+                const float up = __uint_as_float((254u - ex) << 23);  // 2^-(ex - 127)
                 uint32_t o4[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
                 *reinterpret_cast<uint4 *>(smem + PwSmem::kQ + x * 32768 + tc_swz(tr, m, 16384u)) =
                     make_uint4(o4[0], o4[1], o4[2], o4[3]);
                 // the row's factor stays positive, so that a hidden key's -inf times it is -inf
-                if (m == 0) qfs[128 * x + tr] = fmaxf(__uint_as_float(max(ex, 1u) << 23) * p.scale_log2, FLT_MIN);
+                if (m == 0) qfs[128 * x + tr] = fmaxf(__uint_as_float(ex << 23) * p.scale_log2, FLT_MIN);
             }
             fence_async_smem();
             mbar_arrive(q_full);
@@ -287,10 +290,13 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
         const int pos_hi = L - p.n_q + row_pos(min(128 * x + 127, p.rows - 1 - r0));
         const uint64_t ff = pair_of(qf);
         float m_run = -INFINITY, l_run = 0.f;
+        // Every wait's outcome is made warp-uniform: the tensor-memory loads and stores
+        // below are warp-collective.  A warp whose wait gave up still comes to the next
+        // barriers of its pair and says so there, and the two leave together: neither is
+        // left waiting at one.
+        bool left = false, leaves = !ok;
         for (int j = 0; ok && j < T; ++j) {
-            // every wait's outcome is made warp-uniform: the tensor-memory loads
-            // and stores below are warp-collective
-            if (!__all_sync(0xffffffffu, tc_wait(&s_full[x], j & 1, abort_flag))) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, tc_wait(&s_full[x], j & 1, abort_flag))) { ok = false; leaves = true; break; }
             tc_fence_after();
             uint32_t s[32];
             tmem_ld32(t_s, s);
@@ -317,9 +323,10 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
             const bool rise = bar_red_or(pair_bar, 64, tmax > m_run + kTcLazy);
             float alpha = 1.f;
             if (rise) {
-                // some row's max rises, in one of the halves
+                // some row's max rises, in one of the halves, or one of the warps leaves
                 red_row[256 * hf] = tmax;
                 named_sync(pair_bar, 64);
+                if (leave[warp ^ 4]) { ok = false; left = true; break; }
                 tmax = fmaxf(tmax, red_row[256 * (hf ^ 1)]);
                 if (tmax > m_run + kTcLazy) {
                     alpha = ex2(m_run - tmax);  // 0 when m_run was -inf
@@ -346,7 +353,12 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
             l_run += pair_sum(sum2) + pair_sum(sum3);
             // P's columns and O are free once P . V of the last tile is done
             if (j > 0) {
-                if (!__all_sync(0xffffffffu, tc_wait(&pv_done[x], (j - 1) & 1, abort_flag))) { ok = false; break; }
+                // (after the last tile the pair meets at the barrier below)
+                if (!__all_sync(0xffffffffu, tc_wait(&pv_done[x], (j - 1) & 1, abort_flag))) {
+                    ok = false;
+                    leaves = j + 1 < T;
+                    break;
+                }
                 if (rise) {
                     tc_fence_after();
 #pragma unroll
@@ -366,11 +378,19 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
             __syncwarp();  // every lane has stored and fenced its weights
             if (lane == 0) mbar_arrive(&p_full[x]);
         }
-        if (ok && __all_sync(0xffffffffu, tc_wait(o_full, 0, abort_flag))) {
-            tc_fence_after();
-            red_row[256 * hf] = l_run;
+        if (leaves) {
+            (void)bar_red_or(pair_bar, 64, true);
+            if (lane == 0) leave[warp] = 1;
             named_sync(pair_bar, 64);
-            l_run = red_row[0] + red_row[256];
+            left = true;
+        }
+        if (!left) {
+            red_row[512 + 256 * hf] = l_run;
+            named_sync(pair_bar, 64);
+            l_run = red_row[512] + red_row[512 + 256];
+        }
+        if (ok && !left && __all_sync(0xffffffffu, tc_wait(o_full, 0, abort_flag))) {
+            tc_fence_after();
             const float inv = l_run > 0.f ? 1.0f / l_run : 0.f;
             const size_t at = row < p.rows ? out_row(row - r0) * kHeadDim : 0;
 #pragma unroll

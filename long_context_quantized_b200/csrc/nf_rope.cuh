@@ -5,11 +5,11 @@
 //   a_i = position[axis(i)] * inv_freq[i]:  (x, y) -> (x cos - y sin, y cos + x sin).
 // Positions of a long context put a_i at 10^5 radians and more, where an fp32
 // product is off by hundredths of a radian.  So the angle is taken in turns in
-// fp64: a = position * inv_freq is exact (31 + 24 bits; one rounding above
-// 2^53), and its turns a / 2 pi come as an unevaluated sum of two doubles (the
-// product with the leading double of 1 / 2 pi split exactly by an FMA, plus the
-// product with the trailing one); the whole turns are dropped exactly and what
-// is left, at most half a turn, goes to sincospi.  cos and sin are then good to
+// fp64: position * inv_freq as an exact sum of two doubles (a product and, by an
+// FMA, what its rounding left), and its turns, a / 2 pi, as a sum of two doubles
+// again (the product with the leading double of 1 / 2 pi split by an FMA, plus
+// the products with the trailing one); the whole turns are dropped exactly and
+// what is left, at most half a turn, goes to sincospi.  cos and sin are then good to
 // a few units of 2^-53 whatever the position.
 //   Queries are turned in fp32 (cos and sin rounded to fp32 once) and rounded
 // once to their type.  Keys are turned in fp64 and rounded to fp32 once before
@@ -61,9 +61,9 @@ struct RopeParams {
 // cos and sin of position * f, see above.
 __device__ __forceinline__ void rope_angle(int position, float f, double &c, double &s) {
     constexpr double kInv2PiHi = 0x1.45f306dc9c883p-3, kInv2PiLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi) as hi + lo
-    const double a = (double)position * (double)f;
+    const double a = (double)position * (double)f, a_lo = fma((double)position, (double)f, -a);
     const double hi = a * kInv2PiHi;
-    const double lo = fma(a, kInv2PiHi, -hi) + a * kInv2PiLo;
+    const double lo = fma(a, kInv2PiHi, -hi) + fma(a, kInv2PiLo, a_lo * kInv2PiHi);
     const double turn = (hi - rint(hi)) + lo;
     sincospi(2.0 * turn, &s, &c);
 }

@@ -120,15 +120,15 @@ def decode_tolerance(parts):
 
 
 def prefill_tolerance(parts):
-    """The same for the tcgen05 prefill: q and the dequantised K are each
-    rounded to fp16 (a score moves by at most 2 x 2^-11 dk), a weight's exponent
-    is rounded to fp16 (at most 25 in magnitude before the weight itself leaves
-    fp16: 25 x 2^-11 x ln 2), 2^x is good to 2^-9, V is rounded to fp16 once
-    (2^-11); weights reach 2^8 and the running max is within 2^8 of the true
-    one, so the largest weight is at least 1 and what fp16 loses at its bottom
-    is n 2^-25 / sum exp(s - max)."""
-    return ((2 * 2.0 ** -10 * parts["dk"] + 25 * 2.0 ** -11 * math.log(2) + 2.0 ** -9 + 2.0 ** -11 + 2.0 ** -15)
-            * parts["mag"] + parts["spread"] * 2.0 ** -24)
+    """The same for the tcgen05 prefill: q (down to 2^-14 of its row's max exactly,
+    below that by at most 2^-25) and the dequantised K (2^-11) are held in fp16, so a
+    score moves by at most 2^-11 dk + 2^-25 dq, a normalised weight by twice that
+    relatively; the weights and V are rounded to fp16 once each (2 x 2^-11); weights
+    reach 2^8 and the running max is within 2^8 of the true one, so the largest
+    weight is at least 1 and what fp16 loses at its bottom is n 2^-25 / sum exp(s -
+    max).  fp32 sums and exponentials as above."""
+    return ((2 * (2.0 ** -11 * parts["dk"] + 2.0 ** -25 * parts["dq"]) + 2.0 ** -10 + 2.0 ** -15) * parts["mag"]
+            + parts["spread"] * 2.0 ** -24)
 
 
 def check_out(out, ref, tol):

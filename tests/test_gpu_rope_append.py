@@ -122,6 +122,23 @@ def test_far_positions(far):
     c.check()
 
 
+@pytest.mark.parametrize("pos", [2 ** 31 - 1, -2 ** 31, 1073741789])
+def test_angles_at_the_largest_positions(pos):
+    """A key of (1, 0) pairs holds its angles' cos and sin: the fp32 keys of a bf16
+    pool's rows differ from them by their rounding to bf16 alone, and queries of
+    fp32 by 2^-23 -- far below what a rounded product position x frequency leaves
+    (2^-22 radians and more)."""
+    c = Case(nf.NF_KV_BF16, batch=1, n_new=1, dtype=torch.float32, n_axes=1, theta=3.0, strided=False, before=(5,))
+    for x in (c.q, c.k):
+        x.zero_()
+        x[..., :64] = 1.0
+    c.np_pos[:] = pos
+    c.run()
+    want = c.turned(c.q)
+    assert np.abs(c.q_out.double().cpu().numpy() - want).max() <= 2.0 ** -23
+    c.check()
+
+
 @pytest.mark.parametrize("batch, n_new, hq, hkv", [(1, 1, 1, 1), (1, 1, 40, 8), (5, 1, 32, 4), (1, 700, 5, 1), (3, 257, 8, 8)])
 def test_sizes(batch, n_new, hq, hkv):
     for fmt in (nf.NF_KV_K8V4, nf.NF_KV_K4V4):

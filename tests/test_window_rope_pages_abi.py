@@ -51,6 +51,7 @@ def test_prefill_window_takes_only_k8v4_and_bf16(lib):
     for fmt in (nf.NF_KV_K8V8, nf.NF_KV_F8, nf.NF_KV_K4V4, nf.NF_KV_BF16):
         assert _window(lib, "nf_prefill_attn_window", kv=_layer(fmt)) == UNS
     assert _window(lib, "nf_prefill_attn_window", q_dtype=nf.NF_F32) == UNS
+    assert _window(lib, "nf_prefill_attn_window", H_q=2 << 21) == UNS  # above 2^20 q-heads per kv-head
 
 
 def test_window_workspace_size(lib):
@@ -77,7 +78,8 @@ def _rope(lib, **over):
     (dict(batch=-1), INV), (dict(n_new=-1), INV), (dict(H_q=-1), INV), (dict(dtype=nf.NF_F16), UNS), (dict(inv=None), INV),
     (dict(pos=None), INV), (dict(q=None), INV), (dict(k=None), INV), (dict(v=None), INV), (dict(bt=None), INV),
     (dict(before=None), INV), (dict(q_out=None), INV), (dict(max_blocks=0), INV), (dict(k=260), INV), (dict(q_out=260), INV),
-    (dict(ts=770), INV), (dict(bs=2), INV), (dict(dtype=nf.NF_F32, q=264), INV), (dict(batch=2, n_new=1 << 30), INV)])
+    (dict(ts=770), INV), (dict(bs=2), INV), (dict(dtype=nf.NF_F32, q=264), INV), (dict(batch=2, n_new=1 << 30), INV), (dict(batch=70000), UNS),
+    (dict(H_q=1 << 21), INV)])
 def test_rope_refusals(lib, over, status):
     assert _rope(lib, **over) == status
     assert lib.nf_last_error()
