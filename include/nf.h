@@ -434,11 +434,11 @@ nf_status nf_prefill_attn_window(const nf_kv_layer *kv, const void *q, int32_t q
  * positions: int32 [batch][n_new][n_axes], device; any values (they are not
  *   the cache positions, which come from seqlens_before as in
  *   nf_kv_append_quant).
- * q, k_new, v_new: rows of in_dtype (NF_F32 or NF_BF16), element (b, t, head,
- *   c) at data + b * batch_stride + t * token_stride + head * 128 + c, so that
- *   the three parts of a fused projection's output need no copy.  Strides in
- *   elements, multiples of 4; data 16-byte (NF_F32) or 8-byte (NF_BF16)
- *   aligned.
+ * q_k_v: three entries (host, read before the call returns), the rows q, k_new
+ *   and v_new of in_dtype (NF_F32 or NF_BF16), element (b, t, head, c) at data +
+ *   b * batch_stride + t * token_stride + head * 128 + c, so that the three
+ *   parts of a fused projection's output need no copy.  Strides in elements,
+ *   multiples of 4; data 16-byte (NF_F32) or 8-byte (NF_BF16) aligned.
  * q_out: [batch][n_new][num_q_heads][128] of in_dtype; it may be q's own
  *   memory when q is contiguous.  num_q_heads may be 0 (q and q_out unused).
  * n_valid: int32 [batch] (device) or NULL: tokens t >= n_valid[b] are padding;
@@ -465,9 +465,8 @@ typedef struct {
     int64_t batch_stride, token_stride;
 } nf_heads;
 nf_status nf_rope_append_quant(const nf_kv_layer *kv, const nf_rope *rope, const int32_t *positions,
-                               const nf_heads *q, const nf_heads *k_new, const nf_heads *v_new,
-                               int32_t in_dtype, int32_t batch, int32_t n_new, int32_t num_q_heads,
-                               const int32_t *block_table, int32_t max_blocks,
+                               const nf_heads *q_k_v, int32_t in_dtype, int32_t batch, int32_t n_new,
+                               int32_t num_q_heads, const int32_t *block_table, int32_t max_blocks,
                                const int32_t *seqlens_before, const int32_t *n_valid, void *q_out,
                                nf_stream_t stream);
 

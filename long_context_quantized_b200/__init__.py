@@ -1,6 +1,9 @@
 """B200 (sm_100a) decode attention over a K8/V4-quantised, segmented KV cache.
 
-Thin Python binding of ``libnf.so`` (the C ABI declared in ``include/nf.h``).
+Thin Python binding of ``libnf.so`` (the C ABI declared in ``include/nf.h``):
+appending, decode and prefill attention, and for sessions that bound their
+context the windowed forms, rotary positions on the way into the cache and the
+pages of the pool.
 Every function here only marshals torch tensors into pointers and sizes and
 calls the C entry point of the same name; all computation happens in the CUDA
 kernels of ``csrc/``.  torch provides device memory and the current stream.
@@ -11,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 
 import torch
@@ -67,6 +71,9 @@ class nf_heads(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
 
 
+_pack_q_k_v = struct.Struct("@PqqPqqPqq").pack  # three nf_heads, without building ctypes objects
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -116,7 +123,7 @@ def load_library():
         lib.nf_decode_attn_window.restype = I
         lib.nf_prefill_attn_window.argtypes = [P, P, I, I, I, I, P, I, P, I, I, I, F, P, I, P, P]
         lib.nf_prefill_attn_window.restype = I
-        lib.nf_rope_append_quant.argtypes = [P, P, P, P, P, P, I, I, I, I, P, I, P, P, P, P]
+        lib.nf_rope_append_quant.argtypes = [P, P, P, P, I, I, I, I, P, I, P, P, P, P]
         lib.nf_rope_append_quant.restype = I
         lib.nf_kv_reserve.argtypes = lib.nf_kv_release.argtypes = [P, I, P, I, I, P, P, P]
         lib.nf_kv_reserve.restype = lib.nf_kv_release.restype = I
@@ -506,13 +513,13 @@ class Rope:
 
 
 def _heads(where, name, t, dtype, device, shape):
-    """The rows of t [batch][n_new][heads][128], whose heads must be contiguous."""
+    """Address, batch and token stride of t [batch][n_new][heads][128], whose heads must be contiguous."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         _refuse(where, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {dtype} {shape} on cuda:{device}")
     sb, st, sh, sc = t.stride()
     if (sc != 1 or (sh != HEAD_DIM and shape[2] > 1)) and t.numel():
         _refuse(where, f"{name}: the heads of a token must be contiguous")
-    return nf_heads(t.data_ptr(), sb, st)
+    return t.data_ptr(), sb, st
 
 
 def nf_rope_append_quant(kv: KVLayer, rope: Rope, positions, q, k_new, v_new, block_table, seqlens_before, q_out,
@@ -540,7 +547,7 @@ def nf_rope_append_quant(kv: KVLayer, rope: Rope, positions, q, k_new, v_new, bl
         _on(where, "q_out", q_out, d, dtype)
         out = q_out.data_ptr()
     else:
-        H_q, qh, out = 0, nf_heads(None, 0, 0), None
+        H_q, qh, out = 0, (0, 0, 0), None
     _on(where, "positions", positions, d, _i32)
     _on(where, "block_table", block_table, d, _i32)
     if kv.device != d or rope.device != d:
@@ -550,8 +557,8 @@ def nf_rope_append_quant(kv: KVLayer, rope: Rope, positions, q, k_new, v_new, bl
     if block_table.dim() != 2 or block_table.shape[0] != B:
         _refuse(where, "block_table must be [batch][max_blocks] with the inputs' batch")
     st = (_lib or load_library()).nf_rope_append_quant(
-        kv.ref, rope.ref, positions.data_ptr(), ctypes.byref(qh), ctypes.byref(k), ctypes.byref(v), _dtype_code(dtype),
-        B, n_new, H_q, block_table.data_ptr(), block_table.shape[1], _vector(where, "seqlens_before", seqlens_before, d, B),
+        kv.ref, rope.ref, positions.data_ptr(), _pack_q_k_v(*qh, *k, *v), _dtype_code(dtype), B, n_new, H_q,
+        block_table.data_ptr(), block_table.shape[1], _vector(where, "seqlens_before", seqlens_before, d, B),
         None if n_valid is None else _vector(where, "n_valid", n_valid, d, B), out, _call_stream(stream, d))
     if st:
         _check(st, where)
@@ -620,8 +627,8 @@ def nf_kv_copy_blocks(layers: KVLayers, src, dst, stream=None):
     if layers.device != d:
         _refuse(where, f"the pool is on cuda:{layers.device}, src on cuda:{d}")
     n = len(src) if src.dim() == 1 else -1
-    st = (_lib or load_library()).nf_kv_copy_blocks(layers.c, len(layers), _vector(where, "src", src, d, n), _vector(where, "dst", dst, d, n),
-                                          n, _call_stream(stream, d))
+    st = (_lib or load_library()).nf_kv_copy_blocks(layers.c, len(layers), _vector(where, "src", src, d, n),
+                                                    _vector(where, "dst", dst, d, n), n, _call_stream(stream, d))
     if st:
         _check(st, where)
 

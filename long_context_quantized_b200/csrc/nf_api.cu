@@ -829,9 +829,9 @@ nf_status nf_prefill_attn_window(const nf_kv_layer *kv, const void *q, int32_t q
 }
 
 // ---------------------------------------------------------------- rotary positions and append
-nf_status nf_rope_append_quant(const nf_kv_layer *kv, const nf_rope *rope, const int32_t *positions, const nf_heads *q,
-                               const nf_heads *k_new, const nf_heads *v_new, int32_t in_dtype, int32_t batch,
-                               int32_t n_new, int32_t num_q_heads, const int32_t *block_table, int32_t max_blocks,
+nf_status nf_rope_append_quant(const nf_kv_layer *kv, const nf_rope *rope, const int32_t *positions,
+                               const nf_heads *q_k_v, int32_t in_dtype, int32_t batch, int32_t n_new,
+                               int32_t num_q_heads, const int32_t *block_table, int32_t max_blocks,
                                const int32_t *seqlens_before, const int32_t *n_valid, void *q_out,
                                nf_stream_t stream) {
     nf_status st = check_layer(kv);
@@ -850,7 +850,8 @@ nf_status nf_rope_append_quant(const nf_kv_layer *kv, const nf_rope *rope, const
         return fail(NF_ERR_INVALID_ARG, "batch %d / n_new %d / num_q_heads %d < 0", batch, n_new, num_q_heads);
     if (in_dtype != NF_F32 && in_dtype != NF_BF16)
         return fail(NF_ERR_UNSUPPORTED, "in_dtype %d (NF_F32 or NF_BF16)", in_dtype);
-    if (!q || !k_new || !v_new) return fail(NF_ERR_INVALID_ARG, "q / k_new / v_new is NULL");
+    if (!q_k_v) return fail(NF_ERR_INVALID_ARG, "q_k_v is NULL");
+    const nf_heads *q = q_k_v, *k_new = q_k_v + 1, *v_new = q_k_v + 2;
     if ((long long)batch * n_new == 0) return done();
     if (!rope->inv_freq || !positions || !k_new->data || !v_new->data || !block_table || !seqlens_before ||
         (num_q_heads > 0 && (!q->data || !q_out)))

@@ -1055,6 +1055,14 @@ __device__ __forceinline__ void finish_piece_coop(const DecodeParams &p, int s_i
 // its sinks' chunks and its window's (win_span); positions of the work cut
 // count in that list, and each stage maps them to keys.  A sequence of length
 // 0 is an unused row of the batch.
+// What bounds the windowed form (K8/V4, 1 query): few short windows, the chain of
+// a launch -- lengths, cut, table, keys, merge, ticket, final merge -- 8.9 us
+// for 1024 keys of 8 kv-heads; many sequences, the pieces' set-up and merge beside
+// the stream: 64 requests at a 4096-key window 46.5 us, 201 MB, 0.67 of the
+// measured copy rate (148 whole segments, one per CTA, reach 0.77).  The prefix
+// sum of the cut, one walk per piece, the next piece's query rows in registers and
+// the unrolled merge took the 64 requests from 52.4 us.  Two smaller CTAs per SM
+// (96 registers, two 128-key stages) were 10 us slower there.
 template <int NT, bool QF32, int FMT, bool WIN>
 __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
     using ST = Stage<FMT, NT>;

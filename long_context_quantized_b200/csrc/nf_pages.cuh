@@ -15,7 +15,12 @@
 //
 // The bytes are in the copies: a page of 4 kv-heads of K8/V4 is 207 KB per
 // layer.  copy_pages spreads (pair, layer, 16 KB piece) units evenly over the
-// grid; a thread has four 16-byte loads in flight before it stores.
+// grid; a thread has four 16-byte loads in flight before it stores.  Measured:
+// compacting 180 pages x 16 layers (1.19 GB read and written) 207 us, 5.75 TB/s
+// (0.89 of the measured copy rate); forking 32 rows with their cut pages (212 MB)
+// 36 us, 5.85 TB/s.  Eight loads in flight: 202 and 37 us; default caching
+// instead of streaming loads and stores: 210 and 35.  A step's reserve and
+// release of 64 rows take 3 us each, chains of dependent loads of one CTA.
 #pragma once
 
 #include "nf_common.cuh"

@@ -169,9 +169,7 @@ __device__ __forceinline__ void tc_load_v(const PrefillParams &p, const int32_t 
 // 9360 to infinity.  A larger scale is reported as NF_DEVERR_RANGE.
 constexpr uint32_t kTcMaxKScaleBits = 0x6007u;  // 515.5
 constexpr uint32_t kTcMaxVScaleBits = 0x7091u;  // 9352
-// key's dequantised fp16 K row (code x K scale) into an operand whose blocks of
-// 64 channels are BLK bytes apart
-template <uint32_t BLK = 8192u>
+// key's dequantised fp16 K row (code x K scale)
 __device__ __forceinline__ void tc_convert_k(const TcRawK &r, int key, unsigned char *kb) {
     if (r.ok && (r.ks & 0x7FFFu) > kTcMaxKScaleBits) report(NF_DEVERR_RANGE);
     const __half2 sk = u32_h2(r.ok ? (r.ks & 0xFFFFu) * 0x10001u : 0u);
@@ -186,12 +184,11 @@ __device__ __forceinline__ void tc_convert_k(const TcRawK &r, int key, unsigned 
         a.z = h2_u32(__hmul2(u32_h2(a.z), sk)); a.w = h2_u32(__hmul2(u32_h2(a.w), sk));
         c.x = h2_u32(__hmul2(u32_h2(c.x), sk)); c.y = h2_u32(__hmul2(u32_h2(c.y), sk));
         c.z = h2_u32(__hmul2(u32_h2(c.z), sk)); c.w = h2_u32(__hmul2(u32_h2(c.w), sk));
-        *reinterpret_cast<uint4 *>(kb + tc_swz(key, 2 * u, BLK)) = a;
-        *reinterpret_cast<uint4 *>(kb + tc_swz(key, 2 * u + 1, BLK)) = c;
+        *reinterpret_cast<uint4 *>(kb + tc_swz(key, 2 * u, 8192u)) = a;
+        *reinterpret_cast<uint4 *>(kb + tc_swz(key, 2 * u + 1, 8192u)) = c;
     }
 }
 // key's dequantised fp16 V row (code x V scale; 0 past the end)
-template <uint32_t BLK = 8192u>
 __device__ __forceinline__ void tc_convert_v(const TcRawV &r, int key, unsigned char *vb) {
     const uint32_t keep = r.ok ? 0xFFFFFFFFu : 0u;
     if (r.ok) {
@@ -210,7 +207,7 @@ __device__ __forceinline__ void tc_convert_v(const TcRawV &r, int key, unsigned 
         o.y = h2_u32(__hmul2(nib_odd(w), sv));
         o.z = h2_u32(__hmul2(nib_even(w >> 8), sv));
         o.w = h2_u32(__hmul2(nib_odd(w >> 8), sv));
-        *reinterpret_cast<uint4 *>(vb + tc_swz(key, i, BLK)) = o;
+        *reinterpret_cast<uint4 *>(vb + tc_swz(key, i, 8192u)) = o;
     }
 }
 
@@ -547,8 +544,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
     __syncthreads();
     if (warp == 12) {
         // every MMA of the four streams has completed before tensor memory is freed
-        // (a sequence without valid keys issued none)
-        if (lane == 0 && !bad_len) {
+        if (lane == 0) {
             const uint64_t t0 = global_ns();
             while (!mbar_try_wait_sleep(drain, 0, 20000u))
                 if (global_ns() - t0 > kWaitLimitNs) {

@@ -31,6 +31,26 @@
 // Shared memory: Q [2 tiles][2 blocks of 64 channels][128 rows][128 B], K and V
 // [4 stages][2 blocks][64 keys][128 B] each, 128-byte swizzle as in
 // nf_prefill.cuh.
+// What bounds it: a softmax thread's chain per 64-key tile, about 1.1 us -- the wait
+// for S, its load, the pair's barrier, the exponentials (four warps share a
+// sub-partition's MUFU: 1024 cycles of the 2100) and the store of P -- against
+// 0.55 us of MMA work for the two tiles at the measured 1692 TFLOP/s.  Without the
+// exponentials a launch takes 0.90, without the barrier 0.92, without the
+// converters 0.99 of its time.  Measured (32 / 4 heads, one B200, launches back to
+// back): a chunk of 1024 queries at 180224 keys, window 4096, 82 us (0.50 of the
+// 1692 TFLOP/s); a prompt of 8192 with window 2048, 307 us (0.46; a CTA's start
+// and end are 15% of its 45 us).
+// Choices measured on the same two cases:
+//   P in tensor memory, S freed as soon as it is in registers, 16 softmax warps
+//     with 32 columns each: 82 / 307 us.  8 warps with 64 columns: 96 / 384.
+//     P through shared memory, S double-buffered, 8 warps (nf_prefill.cuh's
+//     roles): 123 / 437.  128-key tiles with P over S: 126 / 441.
+//   Waits that sleep until the phase completes: 82; in a try_wait loop 93, which
+//     takes issue slots from the warps that work (issue is 64% busy).
+//   Two threads per converted row: 82; one (four converter warps): 115, its K
+//     conversion takes 1.5 us a tile.
+//   The MMA operands in uniform registers (a whole warp runs the issue loop): 96
+//     instead of 115 before the changes above.
 // Every mbarrier wait is bounded; a time-out records NF_DEVERR_TIMEOUT and every
 // role leaves its loop.
 #pragma once

@@ -34,6 +34,13 @@
 // pieces, take a warp per row, lane l channels 4l .. 4l + 3, the partner channels
 // coming from the lane rot / 8 away).  Values: half a warp per row, lane m
 // channels 8m .. 8m + 7.
+//
+// What bounds it: many tokens, the bytes and the instructions about equally
+// (16384 tokens, 40 + 2 x 8 heads, int8 cache: 84 us, 437 MB, 0.80 of the measured
+// copy rate; issue 76% busy); a chunk of 1024 tokens (32 + 2 x 4 heads) 6.2 us,
+// half of it the latency of one CTA; a step's tokens 2.8 us, a launch.  With one
+// lane per 4 channels and shuffled partners for every row, and IEEE quotients,
+// the 16384 tokens took 207 us.
 #pragma once
 
 #include "nf_append.cuh"

@@ -63,17 +63,17 @@ def test_window_workspace_size(lib):
 def _rope(lib, **over):
     a = dict(kv=_layer(), rot=128, layout=0, n_axes=3, axis=[i % 3 for i in range(64)], inv=256, pos=256, q=256, k=256,
              v=256, bs=768, ts=768, dtype=nf.NF_BF16, batch=1, n_new=1, H_q=2, bt=256, max_blocks=4, before=256, valid=None,
-             q_out=256, rope=True)
+             q_out=256, rope=True, rows=True)
     a.update(over)
     rope = nf.nf_rope(a["rot"], a["layout"], a["n_axes"], (ctypes.c_uint8 * 64)(*a["axis"]), a["inv"])
-    rows = [ctypes.byref(nf.nf_heads(a[x], a["bs"], a["ts"])) for x in ("q", "k", "v")]
+    rows = (nf.nf_heads * 3)(*[nf.nf_heads(a[x], a["bs"], a["ts"]) for x in ("q", "k", "v")])
     return lib.nf_rope_append_quant(None if a["kv"] is None else ctypes.byref(a["kv"]),
-                                    ctypes.byref(rope) if a["rope"] else None, a["pos"], *rows, a["dtype"], a["batch"],
+                                    ctypes.byref(rope) if a["rope"] else None, a["pos"], rows if a["rows"] else None, a["dtype"], a["batch"],
                                     a["n_new"], a["H_q"], a["bt"], a["max_blocks"], a["before"], a["valid"], a["q_out"], None)
 
 
 @pytest.mark.parametrize("over, status", [
-    (dict(kv=None), INV), (dict(rope=False), INV), (dict(rot=4), UNS), (dict(rot=12), UNS), (dict(rot=136), UNS),
+    (dict(kv=None), INV), (dict(rope=False), INV), (dict(rows=False), INV), (dict(rot=4), UNS), (dict(rot=12), UNS), (dict(rot=136), UNS),
     (dict(rot=0), UNS), (dict(layout=2), UNS), (dict(n_axes=0), UNS), (dict(n_axes=5), UNS), (dict(n_axes=2), INV),
     (dict(batch=-1), INV), (dict(n_new=-1), INV), (dict(H_q=-1), INV), (dict(dtype=nf.NF_F16), UNS), (dict(inv=None), INV),
     (dict(pos=None), INV), (dict(q=None), INV), (dict(k=None), INV), (dict(v=None), INV), (dict(bt=None), INV),
