@@ -635,6 +635,7 @@ nf_status run_prefill(const nf_kv_layer *kv, const void *q, int32_t q_dtype, int
         return fail(NF_ERR_INVALID_ARG, "q / out must be 16-byte aligned");
     const long long rows = (long long)(num_q_heads / kv->num_kv_heads) * n_q;
     const long long row_tiles = (rows + nf::kTcRows - 1) / nf::kTcRows;
+    if (win && rows > (1 << 30)) return fail(NF_ERR_UNSUPPORTED, "prefill: %lld query rows per kv-head", rows);
     if (win && num_q_heads / kv->num_kv_heads > (1 << 20))  // the kernel divides by the group in fp32
         return fail(NF_ERR_UNSUPPORTED, "prefill: %d q-heads per kv-head", num_q_heads / kv->num_kv_heads);
     if (rows > 0x7fffffffLL || row_tiles > 0x7fffffffLL)

@@ -105,7 +105,10 @@ def test_decode_window_unused_rows():
             assert not out[0].any() and not out[2].any() and torch.isinf(c.lse[0]).all()
     c = Case(nf.NF_KV_K8V4, [1, 500], n_q=2)
     c.check(64, 4, errors=nf.NF_DEVERR_SEQLEN)  # its rows are zeros too
-    Case(nf.NF_KV_K8V4, [0, 0]).check(64, 4)
+    for fmt in FORMATS:
+        Case(fmt, [0, 0]).check(64, 4)
+        Case(fmt, [0, 0], hq=24).check(64, 4, torch.bfloat16)  # 12 rows a kv-head
+        Case(fmt, [0, 300, 0], hq=24, n_q=2).check(64, 4, torch.bfloat16)
 
 
 def test_decode_window_large_batch():

@@ -52,6 +52,7 @@ def test_prefill_window_takes_only_k8v4_and_bf16(lib):
         assert _window(lib, "nf_prefill_attn_window", kv=_layer(fmt)) == UNS
     assert _window(lib, "nf_prefill_attn_window", q_dtype=nf.NF_F32) == UNS
     assert _window(lib, "nf_prefill_attn_window", H_q=2 << 21) == UNS  # above 2^20 q-heads per kv-head
+    assert _window(lib, "nf_prefill_attn_window", H_q=4, n_q=1 << 30, max_seqlen=1 << 30, max_blocks=1 << 23) == UNS
 
 
 def test_window_workspace_size(lib):
