@@ -343,3 +343,25 @@ def test_window_binding_refusals():
             call(**over)
     torch.cuda.synchronize()
     assert nf.nf_get_device_error() == 0
+
+
+def test_two_streams_at_once():
+    """Decode calls (each with its own workspace) and prefill calls on two streams, not waiting for one another."""
+    mtp = Case(nf.NF_KV_K8V4, [9000, 4000], n_q=4, hq=32, hkv=2, q_seed=6)
+    one = Case(nf.NF_KV_K8V4, [7000, 20, 3000], n_q=1, q_seed=7)
+    chunk = Case(nf.NF_KV_K8V4, [2100], n_q=300, hq=8, hkv=2, q_seed=8)
+    want = [mtp.run(2500, 4), one.run(1000, 300), chunk.run(700, 4, prefill=True)]
+    outs = [[torch.empty_like(w) for _ in range(6)] for w in want]
+    tables = [c.table for c in (mtp, one, chunk)]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for i in range(6):
+        with torch.cuda.stream(a):
+            nf.nf_decode_attn_window(mtp.kv, mtp.q, tables[0], mtp.lens, mtp.max_len, 2500, 4, SCALE, outs[0][i], None, mtp.ws)
+        with torch.cuda.stream(b):
+            nf.nf_decode_attn_window(one.kv, one.q, tables[1], one.lens, one.max_len, 1000, 300, SCALE, outs[1][i], None, one.ws)
+        with torch.cuda.stream(a if i % 2 else b):
+            nf.nf_prefill_attn_window(chunk.kv, chunk.q, tables[2], chunk.lens, chunk.max_len, 700, 4, SCALE, outs[2][i])
+    torch.cuda.synchronize()
+    assert nf.nf_get_device_error() == 0
+    assert all(torch.equal(got, w) for w, row in zip(want, outs) for got in row)
