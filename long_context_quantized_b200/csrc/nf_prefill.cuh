@@ -17,6 +17,8 @@
 //   first.
 #pragma once
 
+#include <cfloat>
+
 #include "nf_common.cuh"
 #include "nf_tc.cuh"
 
@@ -320,7 +322,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
                 for (int e = 0; e < 4; ++e) am = max(am, max((ww[e] << 16) & 0x7FFFFFFFu, ww[e] & 0x7FFF0000u));
             }
             const float amax = __uint_as_float(am);
-            const float inv = amax > 0.f ? 1.0f / amax : 0.f;
+            // The scale's sign goes into the row, so that the row's factor is positive and
+            // a hidden key's -inf times it stays -inf; a row whose max |q| is below 2^-120
+            // (whose inverse may leave fp32) counts as zeros, which moves its scores by
+            // less than 2^-97 of the scale.
+            const float inv = amax > 0x1p-120f ? copysignf(1.0f / amax, p.scale_log2) : 0.f;
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
                 const uint32_t ww[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
                 *reinterpret_cast<uint4 *>(smem + TcSmem::kQ + x * 32768 + tc_swz(t, c, 16384u)) =
                     make_uint4(o4[0], o4[1], o4[2], o4[3]);
             }
-            qfs[128 * x + t] = amax * p.scale_log2;
+            qfs[128 * x + t] = fmaxf(amax * fabsf(p.scale_log2), FLT_MIN);
         }
         fence_async_smem();
         mbar_arrive(q_full);

@@ -153,3 +153,56 @@ def test_prefill_reports_k_outside_fp16_range():
                        w.softmax_scale, True, out, None)
     torch.cuda.synchronize()
     assert nf.nf_get_device_error() == nf.NF_DEVERR_RANGE
+
+
+def _attend(case, scale, causal, q=None, kv_fmt=K8, prefill=True, q_dtype=torch.bfloat16):
+    """(out, lse) of the kernel and of the oracle for one small case at the given softmax scale."""
+    w = workloads.custom("pf_scale", q_dtype=q_dtype, kv_in_dtype=torch.bfloat16, causal=causal, **case)
+    g = gpu_layer(w, 0, kv_fmt, q_override=q, attn="prefill" if prefill else "decode")
+    bt, sl = torch.as_tensor(g["bt"], device="cuda"), torch.tensor(w.seqlens, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(g["out"], 7.0), torch.full_like(g["lse"], 7.0)
+    if prefill:
+        nf.nf_prefill_attn(g["kv"], g["q"], bt, sl, max(w.seqlens), scale, causal, out, lse)
+    else:
+        ws = torch.zeros(nf.nf_decode_attn_workspace_size(w.batch, w.n_q, w.num_q_heads, w.num_kv_heads, max(w.seqlens)),
+                         dtype=torch.uint8, device="cuda")
+        nf.nf_decode_attn(g["kv"], g["q"], bt, sl, max(w.seqlens), scale, causal, out, lse, ws)
+    torch.cuda.synchronize()
+    assert nf.nf_get_device_error() == 0
+    pool, _ = oracle_pool(w, kv_fmt, g["kvin"], g["bt"])
+    ref_o, ref_l = oracle.decode_attn(pool, g["q"].float().cpu().numpy().astype(np.float64), g["bt"],
+                                      np.array(w.seqlens, np.int32), scale, causal, nthreads=os.cpu_count())
+    return out, lse, ref_o.reshape(out.shape), ref_l.reshape(lse.shape)
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_prefill_zero_and_tiny_query_rows(causal):
+    """A row of zeros weighs every key it sees alike; a row of subnormals too."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    q = torch.randn((1, 70, 8, 128), generator=gen, device="cuda").bfloat16()
+    q[0, 3] = 0
+    q[0, 69, 1] = 0
+    q[0, 4] = 1e-39
+    q[0, 5, :, ::2] = 0
+    q[0, 5, :, 1::2] = -1e-40
+    q[0, 6] *= 1e-30
+    case = dict(cached=(200,), n_new=70, n_q=70, num_q_heads=8, num_kv_heads=2)
+    check_attention(*_attend(case, 128 ** -0.5, causal, q))
+    check_attention(*_attend(case, 1e-20, causal, q))  # max |q| x scale below fp32's range
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.088, -1e-30], ids=["zero", "negative", "tiny"])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_prefill_softmax_scale_of_zero_or_below(scale, causal):
+    """Any finite scale is an argument of the full-context calls."""
+    check_attention(*_attend(dict(cached=(300, 77), n_new=40, n_q=40, num_q_heads=8, num_kv_heads=2), scale, causal))
+
+
+@pytest.mark.parametrize("fmt", [nf.NF_KV_K8V4, nf.NF_KV_BF16, nf.NF_KV_K8V8, nf.NF_KV_F8, nf.NF_KV_K4V4],
+                         ids=["k8v4", "bf16", "k8v8", "f8", "k4v4"])
+@pytest.mark.parametrize("n_q, heads", [(1, 8), (3, 32), (6, 32)])
+@pytest.mark.parametrize("scale", [0.0, -0.088], ids=["zero", "negative"])
+def test_decode_softmax_scale_of_zero_or_below(fmt, n_q, heads, scale):
+    check_attention(*_attend(dict(cached=(700, 90), n_new=n_q, n_q=n_q, num_q_heads=heads, num_kv_heads=4), scale, True,
+                             kv_fmt=fmt, prefill=False))
