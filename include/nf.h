@@ -350,9 +350,10 @@ nf_status nf_attn_combine_packed(const float *parts, int32_t n_splits, int32_t r
  *   recorded as NF_DEVERR_RANGE (and the affected outputs are not finite);
  *   nf_decode_attn has no such limit.
  * Numerics: each query row is scaled to max |q| = 1 and rounded to fp16 once
- *   (a row whose max |q| is at most 2^-120 counts as zeros); K and V are dequantised to fp16 (code x scale, one rounding each); the
- *   softmax weights are rounded to fp16; products accumulate in fp32 on the
- *   5th-generation tensor cores (tcgen05.mma kind::f16, M = 128).
+ *   (a row whose max |q| is at most 2^-120 counts as zeros); K and V are
+ *   dequantised to fp16 (code x scale, one rounding each); the softmax weights
+ *   are rounded to fp16; products accumulate in fp32 on the 5th-generation
+ *   tensor cores (tcgen05.mma kind::f16, M = 128).
  * Device errors: NF_DEVERR_SEQLEN (the sequence's rows come out o = 0,
  *   lse = -inf), NF_DEVERR_BLOCK_ID (that tile's keys read as zeros),
  *   NF_DEVERR_RANGE (see above).

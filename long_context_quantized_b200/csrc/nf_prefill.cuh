@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
 
     if (bad_len) {
         if (threadIdx.x == 0 && rt == p.row_tiles - 1 && h == 0) report(NF_DEVERR_SEQLEN);
+        if (threadIdx.x < 4) mbar_arrive(drain);  // no MMA is issued: the end has nothing to wait for
         for (int idx = threadIdx.x; idx < kTcRows * kHeadDim; idx += kTcThreads) {
             const int r = r0 + idx / kHeadDim, ch = idx % kHeadDim;
             if (r >= p.rows) continue;

@@ -206,3 +206,30 @@ def test_prefill_softmax_scale_of_zero_or_below(scale, causal):
 def test_decode_softmax_scale_of_zero_or_below(fmt, n_q, heads, scale):
     check_attention(*_attend(dict(cached=(700, 90), n_new=n_q, n_q=n_q, num_q_heads=heads, num_kv_heads=4), scale, True,
                              kv_fmt=fmt, prefill=False))
+
+
+def test_prefill_invalid_lengths_do_not_wait():
+    """Sequences of invalid length (0 among them: padding rows of a batch) take no longer than others: many
+    waves of their CTAs end in far less than one bounded wait of two seconds."""
+    w = workloads.custom("pf_pad", cached=(100, 40, 40, 40), n_new=300, n_q=300, num_q_heads=32, num_kv_heads=4,
+                         q_dtype=torch.bfloat16, kv_in_dtype=torch.bfloat16, causal=True)
+    g = gpu_layer(w, 0, K8, attn="prefill")
+    bt = torch.as_tensor(g["bt"], device="cuda")
+    sl = torch.tensor([400, 0, 299, 341], dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(g["out"], 7.0), torch.zeros_like(g["lse"])
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    nf.nf_prefill_attn(g["kv"], g["q"], bt, sl, 340, w.softmax_scale, True, out, lse)
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) < 500.0
+    assert nf.nf_get_device_error() == nf.NF_DEVERR_SEQLEN
+    assert not out.any() and torch.isneginf(lse).all()  # 400 and 341 are above max_seqlen
+    start.record()
+    nf.nf_prefill_attn(g["kv"], g["q"], bt, sl, 400, w.softmax_scale, True, out, lse)
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) < 500.0
+    assert nf.nf_get_device_error() == nf.NF_DEVERR_SEQLEN
+    assert torch.equal(out[0], g["out"][0]) and torch.equal(lse[0], g["lse"][0])
+    assert not out[1:3].any() and torch.isneginf(lse[1:3]).all() and out[3].any()
