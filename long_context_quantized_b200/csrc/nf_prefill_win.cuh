@@ -379,8 +379,8 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
                     leaves = j + 1 < T;
                     break;
                 }
+                tc_fence_after();  // the stores below come after the MMA's reads of P and O
                 if (rise) {
-                    tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t o[16];

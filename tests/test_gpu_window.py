@@ -237,6 +237,16 @@ def test_prefill_window_zero_and_tiny_queries():
     c.check(200, 4, prefill=True)
 
 
+def test_prefill_window_flat_scores_repeat_bitwise():
+    """Scores so close that no running max rises behind the first tile: each tile's weights replace the last
+    one's in tensor memory with no rescale of the output between them."""
+    c = Case(nf.NF_KV_K8V4, [2900, 1500], n_q=300)
+    c.kv = ref.filled_pool(nf.NF_KV_K8V4, c.kv.num_blocks, 2, k_gain=0.02)
+    want = c.check(2500, 4, prefill=True)
+    outs = [c.run(2500, 4, prefill=True) for _ in range(8)]
+    assert all(torch.equal(o, want) for o in outs)
+
+
 def test_prefill_window_errors():
     c = Case(nf.NF_KV_K8V4, [9, 500], n_q=10)
     c.check(64, 4, prefill=True, errors=nf.NF_DEVERR_SEQLEN)
