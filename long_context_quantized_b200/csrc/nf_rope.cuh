@@ -80,7 +80,8 @@ template <bool F32>
 struct Quad {
     float4 v;
     __device__ __forceinline__ void load(const void *base, long long elem) {
-        v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + elem));
+        // (an ordinary load: q_out may be q's memory, which this launch then writes)
+        v = *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + elem);
     }
     __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w; }
     static __device__ __forceinline__ void put(void *base, long long elem, const float (&x)[4]) {

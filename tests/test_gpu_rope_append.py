@@ -171,6 +171,18 @@ def test_in_place_and_without_queries():
     d.check()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("layout", [nf.NF_ROPE_HALVES, nf.NF_ROPE_PAIRS])
+def test_in_place_equals_out_of_place(dtype, layout):
+    """Rows of a token in flight (several a half-warp, and over several CTAs) while others are written over q."""
+    for n_new, hq, rot in ((300, 64, 96), (1, 40, 128)):
+        c = Case(n_new=n_new, hq=hq, rot=rot, layout=layout, dtype=dtype, strided=False)
+        c.run()
+        want = c.q_out.clone()
+        c.run(q_out=c.q)
+        assert torch.equal(c.q, want)
+
+
 def test_position_zero_is_the_plain_append():
     c = Case(n_axes=1, n_new=30, strided=False)
     c.np_pos[:] = 0
