@@ -158,6 +158,13 @@ def _check(st: int, where: str):
         raise NfError(st, where, lib.nf_last_error().decode() or lib.nf_status_string(st).decode())
 
 
+def _int32(where: str, *values):
+    """Refuses integers that ctypes would cut to their low 32 bits."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7FFFFFFF:
+            raise NfError(NF_ERR_INVALID_ARG, where, f"{v} is outside the range of a 32-bit integer")
+
+
 def _dptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -259,6 +266,7 @@ def nf_kv_append_quant(kv: KVLayer, k_new, v_new, block_table, seqlens_before, s
 def nf_decode_attn_workspace_size(batch, n_q, num_q_heads, num_kv_heads, max_seqlen, num_sms=None):
     if num_sms is None:
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    _int32("nf_decode_attn_workspace_size", batch, n_q, num_q_heads, num_kv_heads, max_seqlen, num_sms)
     return int(load_library().nf_decode_attn_workspace_size(batch, n_q, num_q_heads, num_kv_heads,
                                                             max_seqlen, num_sms))
 
@@ -279,6 +287,7 @@ def nf_decode_attn_ex(kv: KVLayer, q, block_table, seqlens, max_seqlen: int, sof
                       _name="nf_decode_attn_ex"):
     """nf_decode_attn with flags (NF_DECODE_EARLY_KV: see nf.h for the caller's
     guarantee)."""
+    _int32(_name, max_seqlen, flags)
     _need(q, "q")
     _need(block_table, "block_table", torch.int32)
     _need(seqlens, "seqlens", torch.int32)
@@ -302,6 +311,7 @@ def nf_prefill_attn(kv: KVLayer, q, block_table, seqlens, max_seqlen: int, softm
     """Chunked-prefill attention (see nf.h): the n_q queries of each sequence
     at positions L - n_q .. L - 1 against its K8/V4 cache; q bf16
     [batch][n_q][H_q][128], out fp32 of the same shape."""
+    _int32("nf_prefill_attn", max_seqlen)
     _need(q, "q")
     _need(block_table, "block_table", torch.int32)
     _need(seqlens, "seqlens", torch.int32)
@@ -323,6 +333,7 @@ def nf_decode_attn_noalloc(kv: KVLayer, q, block_table, seqlens, max_seqlen: int
     """nf_decode_attn for callers that cannot allocate device memory at call
     time: the scratch is a fixed array inside libnf's device image (see nf.h).
     Calls on one device share it, so do not overlap them on the GPU."""
+    _int32("nf_decode_attn_noalloc", max_seqlen)
     _need(q, "q")
     _need(block_table, "block_table", torch.int32)
     _need(seqlens, "seqlens", torch.int32)
@@ -351,11 +362,13 @@ def nf_attn_combine(part_o, part_lse, out, out_lse=None, stream=None):
 def nf_attn_packed_slot_floats(rows: int, head_dim: int = HEAD_DIM) -> int:
     """Floats of one packed split slot: o [rows][head_dim] then lse [rows],
     rounded up to a multiple of 4 (see nf.h)."""
+    _int32("nf_attn_packed_slot_floats", rows, head_dim)
     return int(load_library().nf_attn_packed_slot_floats(int(rows), int(head_dim)))
 
 
 def nf_attn_combine_packed(parts, rows: int, out, out_lse=None, stream=None):
     """parts fp32 [S][slot] (packed split slots) -> out [rows][d], out_lse [rows]."""
+    _int32("nf_attn_combine_packed", rows)
     _need(parts, "parts", torch.float32)
     _need(out, "out", torch.float32)
     _need(out_lse, "out_lse", torch.float32)
@@ -384,6 +397,7 @@ def nf_status_string(status: int) -> str:
 def nf_selftest_bounded_wait(limit_us: int, stream=None):
     """Run the bounded-wait self-test (see nf.h); afterwards
     nf_get_device_error() returns NF_DEVERR_TIMEOUT."""
+    _int32("nf_selftest_bounded_wait", limit_us)
     _check(load_library().nf_selftest_bounded_wait(int(limit_us), _stream(stream)), "nf_selftest_bounded_wait")
 
 
@@ -435,6 +449,7 @@ def _call_stream(stream, device: int):
 def nf_decode_attn_window_workspace_size(batch, n_q, num_q_heads, num_kv_heads, max_seqlen, num_sms=None):
     if num_sms is None:
         num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    _int32("nf_decode_attn_window_workspace_size", batch, n_q, num_q_heads, num_kv_heads, max_seqlen, num_sms)
     return int(load_library().nf_decode_attn_window_workspace_size(batch, n_q, num_q_heads, num_kv_heads, max_seqlen,
                                                                    num_sms))
 
@@ -469,6 +484,7 @@ def nf_decode_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int,
     sees the keys t <= P with t > P - window or t < n_sink (see nf.h).  out
     (fp32 or bf16) has the shape of q [batch][n_q][H_q][128]; seqlens 0 marks an
     unused row of the batch."""
+    _int32("nf_decode_attn_window", max_seqlen, window, n_sink)
     (B, n_q, H_q, _), d, lens, lse = _window_args("nf_decode_attn_window", kv, q, block_table, seqlens, out, out_lse)
     if workspace is None:
         raise NfError(NF_ERR_WORKSPACE, "nf_decode_attn_window", "workspace tensor required "
@@ -487,6 +503,7 @@ def nf_prefill_attn_window(kv: KVLayer, q, block_table, seqlens, max_seqlen: int
                            softmax_scale: float, out, out_lse=None, stream=None):
     """Chunked-prefill attention with a sliding window and sinks (see nf.h and
     nf_decode_attn_window): bf16 q over a K8/V4 pool, out fp32 or bf16."""
+    _int32("nf_prefill_attn_window", max_seqlen, window, n_sink)
     (B, n_q, H_q, _), d, lens, lse = _window_args("nf_prefill_attn_window", kv, q, block_table, seqlens, out, out_lse)
     st = (_lib or load_library()).nf_prefill_attn_window(
         kv.ref, q.data_ptr(), _dtype_code(q.dtype), B, n_q, H_q, block_table.data_ptr(), block_table.shape[1], lens,
@@ -502,6 +519,7 @@ class Rope:
     of the channel pairs (see nf_rope in nf.h)."""
 
     def __init__(self, inv_freq, axis=None, n_axes: int = 1, layout: int = NF_ROPE_HALVES):
+        _int32("Rope", n_axes, layout)
         _need(inv_freq, "inv_freq", torch.float32)
         half = inv_freq.numel()
         axis = [0] * half if axis is None else [int(a) for a in axis]
@@ -635,6 +653,7 @@ def nf_kv_copy_blocks(layers: KVLayers, src, dst, stream=None):
 
 def nf_kv_pages_workspace_size(num_blocks: int, n_forks: int = 0) -> int:
     """Bytes of workspace of nf_kv_fork (n_forks pairs) and nf_kv_compact."""
+    _int32("nf_kv_pages_workspace_size", num_blocks, n_forks)
     return int(load_library().nf_kv_pages_workspace_size(num_blocks, n_forks))
 
 

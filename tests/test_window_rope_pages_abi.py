@@ -136,3 +136,33 @@ def test_binding_refusals_without_a_device():
         nf.Rope(torch.ones(8), n_axes=1)  # not on a device
     with pytest.raises(nf.NfError):
         nf.KVLayers([])
+
+
+@pytest.mark.parametrize("wide", [2 ** 31, 2 ** 32 + 16, 2 ** 63, -2 ** 31 - 1])
+def test_integers_outside_32_bits_are_refused(wide):
+    """ctypes keeps an integer's low 32 bits: a window of 2^32 + 16 would run as one of 16.  Refused before
+    anything else is looked at."""
+    def window(f, *ws):
+        for ints in ((wide, 16, 4), (1000, wide, 4), (1000, 16, wide)):
+            with pytest.raises(nf.NfError) as e:
+                f(None, None, None, None, *ints, 0.1, None, None, *ws)
+            assert e.value.status == INV and str(wide) in str(e.value)
+
+    window(nf.nf_decode_attn_window, None)
+    window(nf.nf_prefill_attn_window)
+    sizes = (1, 1, 32, 4, 1000, 148)
+    calls = [lambda: nf.nf_decode_attn(None, None, None, None, wide, 0.1, True, None),
+             lambda: nf.nf_decode_attn_ex(None, None, None, None, 1000, 0.1, True, wide, None),
+             lambda: nf.nf_decode_attn_noalloc(None, None, None, None, wide, 0.1, True, None),
+             lambda: nf.nf_prefill_attn(None, None, None, None, wide, 0.1, True, None),
+             lambda: nf.nf_attn_packed_slot_floats(wide), lambda: nf.nf_attn_packed_slot_floats(8, wide),
+             lambda: nf.nf_attn_combine_packed(None, wide, None), lambda: nf.nf_selftest_bounded_wait(wide),
+             lambda: nf.nf_kv_pages_workspace_size(wide), lambda: nf.nf_kv_pages_workspace_size(8, wide),
+             lambda: nf.Rope(None, n_axes=wide), lambda: nf.Rope(None, layout=wide)]
+    for i in range(6):
+        for f in (nf.nf_decode_attn_workspace_size, nf.nf_decode_attn_window_workspace_size):
+            calls.append(lambda f=f, i=i: f(*sizes[:i], wide, *sizes[i + 1:]))
+    for call in calls:
+        with pytest.raises(nf.NfError) as e:
+            call()
+        assert e.value.status == INV and str(wide) in str(e.value)
