@@ -169,7 +169,12 @@ def _dptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-_current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
+def _raw_stream(device: int) -> int:
+    # looked up at the call: a torch built without CUDA lacks it, and imports this package for its host logic
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _stream(stream):

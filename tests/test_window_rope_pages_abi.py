@@ -166,3 +166,15 @@ def test_integers_outside_32_bits_are_refused(wide):
         with pytest.raises(nf.NfError) as e:
             call()
         assert e.value.status == INV and str(wide) in str(e.value)
+
+
+def test_package_imports_on_a_torch_without_cuda():
+    """Shard plans and the CPU tests need no CUDA build, which is what has the raw stream lookup."""
+    import os
+    import subprocess
+    import sys
+    code = ("import torch; del torch._C._cuda_getCurrentRawStream; "
+            "import long_context_quantized_b200.sharded as s; print(s.local_pool_table.__name__)")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "local_pool_table" in done.stdout, done.stderr
