@@ -144,8 +144,10 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const Reser
             e1 = min(e1, p.max_blocks);
         }
     };
-    for (int row0 = 0; row0 < p.rows; row0 += kPlanThreads) {
-        const int nrow = min(kPlanThreads, p.rows - row0);
+    // rows of one pass: their pages, at most 2^23 a row, are counted in 32 bits
+    const int pass = min(kPlanThreads, 0x7fffffff / p.max_blocks);
+    for (int row0 = 0; row0 < p.rows; row0 += pass) {
+        const int nrow = min(pass, p.rows - row0);
         for (int r = warp; r < nrow; r += kPlanThreads / 32) {
             int e0, e1, n = 0;
             range(row0 + r, e0, e1);

@@ -90,6 +90,21 @@ def test_reserve_errors():
     assert nf.nf_get_device_error() == nf.NF_DEVERR_POOL
 
 
+def test_reserve_counts_more_than_two_to_the_31_pages():
+    """256 rows of the largest width ask for 2^31 pages between them: the free blocks go to the first row, and
+    the call says that they ran out."""
+    rows, width = 256, 1 << 23
+    table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
+    r = dev([0, 1, 0, 0, 1, 0])
+    nf.nf_kv_reserve(r, table, dev([0] * rows), dev([2 ** 31 - 1] * rows))
+    torch.cuda.synchronize()
+    assert nf.nf_get_device_error() == nf.NF_DEVERR_POOL
+    assert r.tolist() == [1] * 6
+    assert table[0, :4].tolist() == [0, 2, 3, 5]
+    table[0, :4] = -1
+    assert all(bool((part == -1).all()) for part in table.split(16))
+
+
 def test_reserve_on_an_unaligned_view():
     refs = torch.zeros(21, dtype=torch.int32, device="cuda")[1:]
     refs[::3] = 1
