@@ -1487,7 +1487,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
         }
 
         // ---- merge the consumer warps of each row group (shared memory)
-        if (NT != 1) {
+        if (NT != 1 && WIN) {
             nx = walk;
             more = nx.next();
         }
@@ -1561,6 +1561,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
             }
         }
         named_sync(1, kConsumerWarps * 32);
+        // With two row tiles the walk ahead costs registers over the merge, and which side of
+        // it is cheaper is the compiler's: at 64 rows, 180224 keys, before / behind it, full
+        // context K8/V4 145 / 138 us (RK4V4-E8 205 / 200, others alike), a 32768-key window
+        // bf16 76 / 79 us (RK4V4-E8 72 / 74).
+        if (NT != 1 && !WIN) {
+            nx = walk;
+            more = nx.next();
+        }
         finish_piece_single<kConsumerWarps * 32, 1, WIN>(p, s_id, first, n_pieces, rows_here, b, h, !more, smem,
                                                     NS * ST::kStride, fin_bar, fin_phase, sm_o, SM::kMergeFloats,
                                                     misc);
