@@ -247,6 +247,74 @@ def test_prefill_window_flat_scores_repeat_bitwise():
     assert all(torch.equal(o, want) for o in outs)
 
 
+def climb(c, spacing, step=9.0):
+    """Fills the case's pool with keys whose scores (in powers of two) climb by `step` at every `spacing`-th key
+    and stay at that level or up to 2 below until the next: the keys before a rise weigh about as much as the key
+    that brings it, so a row whose last key comes soon behind a rise shows how the earlier sums were rescaled.
+    The rises fall on the first and the second half of 64 keys in turn.  Query head g of a group takes gain
+    (1, 0.5, -1, 1.8)[g % 4] of the climb."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(11)
+    B, _, hq, _ = c.q.shape
+    hkv = c.kv.num_kv_heads
+    u = torch.randn((hkv, 128), generator=gen, device="cuda")
+    for b, L in enumerate(c.seqlens):
+        if L == 0:
+            continue
+        t = torch.arange(L, device="cuda")
+        k_of = torch.zeros(L, device="cuda")
+        for n, at in enumerate(range(spacing, L, spacing)):
+            k_of[at // 64 * 64 + 32 * (n % 2) + at % 32:] += 1.0
+        dip = 2.0 * torch.rand((L,), generator=gen, device="cuda")
+        rise = torch.zeros(L, dtype=torch.bool, device="cuda")
+        rise[1:] = k_of[1:] > k_of[:-1]
+        level = step * (k_of - k_of.mean()) - torch.where(rise, torch.zeros_like(dip), dip)
+        g = level / (SCALE * math.log2(math.e) * 128)
+        k = g[:, None, None] * u + 0.02 * torch.randn((L, hkv, 128), generator=gen, device="cuda")
+        v = torch.randn((1, L, hkv, 128), generator=gen, device="cuda")
+        nf.nf_kv_append_quant(c.kv, k[None].contiguous(), v, c.table[b:b + 1].contiguous(),
+                              torch.zeros(1, dtype=torch.int32, device="cuda"))
+    gain = torch.tensor([1.0, 0.5, -1.0, 1.8], device="cuda").repeat(hq)[:hq // hkv]
+    rows = (u[:, None] * gain[:, None]).reshape(hq, 128)
+    c.q = (rows + 0.05 * torch.randn(c.q.shape, generator=gen, device="cuda")).to(c.q.dtype).contiguous()
+
+
+@pytest.mark.parametrize("window, n_sink", [(3000, 0), (1000, 70)])
+def test_prefill_window_rising_scores(window, n_sink):
+    """The running max rises by more than 2^8 several times: weights, sums and output are rescaled each time."""
+    c = Case(nf.NF_KV_K8V4, [2900, 1300], n_q=700)
+    climb(c, 450)
+    c.check(window, n_sink, torch.bfloat16, prefill=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n_q, hq", [(1, 8), (4, 8), (8, 16)])
+def test_decode_window_rising_scores(fmt, n_q, hq):
+    """The same on every decode kernel, with about a whole segment for each CTA."""
+    rng = np.random.default_rng(5)
+    c = Case(fmt, [int(n) for n in rng.integers(500, 1100, 80)], n_q=n_q, hq=hq)
+    climb(c, 150)
+    c.check(1000, 3, torch.bfloat16)
+
+
+@pytest.mark.parametrize("plane, bits, error", [
+    ("k", 0x6007, 0), ("k", 0x6008, nf.NF_DEVERR_RANGE), ("v", 0x7091, 0), ("v", 0x7092, nf.NF_DEVERR_RANGE)])
+def test_prefill_window_range_of_scales(plane, bits, error):
+    """The largest K and V scales whose codes stay in fp16 (515.5 and 9352) pass, the next ones are reported, on a
+    key that some query sees; a hidden key's scale is not looked at."""
+    window, n_sink = 300, 5
+    for t, err in ((1100, error), (600, 0)):
+        c = Case(nf.NF_KV_K8V4, [1200], n_q=20)
+        page, slot = int(c.np_table[0, t // 256]), t % 256
+        codes, scales, fill = (c.kv.k_codes, c.kv.k_scales, 127) if plane == "k" else (c.kv.v_codes, c.kv.v_scales, 0x77)
+        codes[page, :, slot] = fill
+        scales.view(torch.int16)[page, :, slot] = bits
+        out = c.run(window, n_sink, prefill=True)
+        assert nf.nf_get_device_error() == err
+        if not err:
+            assert torch.isfinite(out).all()
+
+
 def test_prefill_window_errors():
     c = Case(nf.NF_KV_K8V4, [9, 500], n_q=10)
     c.check(64, 4, prefill=True, errors=nf.NF_DEVERR_SEQLEN)
