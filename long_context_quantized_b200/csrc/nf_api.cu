@@ -452,8 +452,13 @@ nf_status nf_kv_append_quant(const nf_kv_layer *kv, const void *k_new, const voi
     const long long items = (long long)batch * n_new * kv->num_kv_heads;
     const long long blocks = (items + 7) / 8;
     if (blocks > 0x7fffffffLL) return fail(NF_ERR_INVALID_ARG, "too many tokens in one append");
-    const cudaError_t e = launch_pdl(nf::append_quant_kernel, (unsigned)blocks, 256, 0,
-                                     reinterpret_cast<cudaStream_t>(stream), p);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto go = [&](void (*kernel)(nf::AppendParams)) { return launch_pdl(kernel, (unsigned)blocks, 256, 0, s, p); };
+    const cudaError_t e = kv->fmt == NF_KV_K8V4   ? go(nf::append_quant_kernel<NF_KV_K8V4>)
+                          : kv->fmt == NF_KV_K8V8 ? go(nf::append_quant_kernel<NF_KV_K8V8>)
+                          : kv->fmt == NF_KV_F8   ? go(nf::append_quant_kernel<NF_KV_F8>)
+                          : kv->fmt == NF_KV_K4V4 ? go(nf::append_quant_kernel<NF_KV_K4V4>)
+                                                  : go(nf::append_quant_kernel<NF_KV_BF16>);
     if (e != cudaSuccess) return fail(NF_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(e));
     return after_launch("append kernel launch");
 }

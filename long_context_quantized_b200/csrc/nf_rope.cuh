@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, F32 ? 6 : 8) rope_append_kern
                         x[e] = (float)fma((double)x[e], c64[f], (PAIRS ? (e & 1) != 0 : second) ? z : -z);
                     }
                 }
-                store_k_row(a, x, lane, s0 + (size_t)j * kBlock);
+                store_k_row<FMT>(a, x, lane, s0 + (size_t)j * kBlock);
             }
             if (t + kRopeWarps < k1) load_kv(t + kRopeWarps);
             continue;
