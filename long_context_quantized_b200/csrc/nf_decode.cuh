@@ -1307,8 +1307,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
     while (piece) {
         const int b = walk.pb, h = walk.ph;
         const int L = seqL[b];  // (read once at the start; 0 for a sequence with no valid key)
-        // the next piece (its stages may be in the ring when this one ends); with 16
-        // rows a warp holds too many registers to carry it through the keys
+        // the next piece (its stages may be in the ring when this one ends), for its query
+        // rows; where it is not carried through the keys it is found again at the end
         PieceWalker nx = walk;
         bool more = nx.next();
         // query fragments of this (sequence, kv-head): lane (g, t) holds row g of
@@ -1561,11 +1561,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
             }
         }
         named_sync(1, kConsumerWarps * 32);
-        // With two row tiles the walk ahead costs registers over the merge, and which side of
-        // it is cheaper is the compiler's: at 64 rows, 180224 keys, before / behind it, full
-        // context K8/V4 145 / 138 us (RK4V4-E8 205 / 200, others alike), a 32768-key window
-        // bf16 76 / 79 us (RK4V4-E8 72 / 74).
-        if (NT != 1 && !WIN) {
+        // Full context: the next piece is walked to again here.  Carried through the keys it
+        // costs the stream (K8/V4, 40 / 8 heads: 524288 keys 136.9 us, here 134.6; 262144 keys
+        // 70.2, 69.7; 64 requests of 2600 keys 34.7, 34.8; 1024 keys 8.99, 9.16), and found
+        // ahead of the merge the many rows (64 rows at 180224 keys: 145, here 137).  Windowed
+        // calls, with fewer keys a piece, carry it, or with 16 rows find it ahead of the
+        // merge (bf16, 64 rows, window 32768: 75, here 79).
+        if (!WIN) {
             nx = walk;
             more = nx.next();
         }
