@@ -1350,8 +1350,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) decode_kernel(const __grid_
                 for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                 if (F8) {
                     // q = s (hi + lo), s = max|q|: |q / s| <= 1 stays inside fp16,
-                    // hi = fp16(q / s), lo = fp16(q / s - hi)
-                    const float inv = amax > 0.f ? 1.0f / amax : 0.f;
+                    // hi = fp16(q / s), lo = fp16(q / s - hi); a row below 2^-120, whose 1 / s
+                    // may leave fp32, counts as zeros (its scores move by less than 2^-97 of
+                    // the scale)
+                    const float inv = amax > 0x1p-120f ? 1.0f / amax : 0.f;
                     float y[4], hi[4], lo[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {

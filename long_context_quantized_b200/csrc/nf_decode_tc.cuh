@@ -634,8 +634,9 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
                     };
                     if constexpr (F8) {
                         // q ~= s (p1 + p2 / 16 + p3 / 256), s = max|q|: each part the
-                        // e4m3 rounding of what the earlier parts leave (times 16)
-                        const float inv = amax > 0.f ? 1.0f / amax : 0.f;
+                        // e4m3 rounding of what the earlier parts leave (times 16); rows
+                        // below 2^-120 count as zeros, as in decode_kernel
+                        const float inv = amax > 0x1p-120f ? 1.0f / amax : 0.f;
                         float y[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[e] = x[e] * inv;

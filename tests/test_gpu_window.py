@@ -168,6 +168,22 @@ def test_decode_window_zero_and_tiny_queries():
         c.check(200, 4)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n_q, hq", [(1, 8), (4, 8), (8, 16)])
+def test_decode_window_tiny_queries_of_every_format(fmt, n_q, hq):
+    """Rows of zeros and of subnormals, channels of zeros among them, whose inverse is no fp32 number."""
+    for dtype in (torch.float32, torch.bfloat16):
+        c = Case(fmt, [600, 90], n_q=n_q, hq=hq, dtype=dtype)
+        c.q[0, 0, 0] = 0
+        c.q[0, 0, 1] = 1e-39
+        c.q[0, 0, 2] = 0
+        c.q[0, 0, 2, ::3] = -2e-40
+        c.q[0, 0, 3] *= 1e-36
+        c.q[1, 0, 0] = 2e-38
+        c.q[1, 0, 1] *= 1e-30
+        c.check(200, 4)
+
+
 def test_decode_window_bad_pages_are_reported():
     c = Case(nf.NF_KV_K8V4, [900])
     c.np_table[0, 2] = 10 ** 6
