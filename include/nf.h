@@ -72,8 +72,9 @@ typedef int32_t nf_status;
 #define NF_DEVERR_TIMEOUT 4   /* a bounded wait inside a kernel gave up (the kernel returned) */
 #define NF_DEVERR_INTERNAL 5  /* a launch-time invariant of the kernel failed (e.g. shared-memory
                                  alignment); the call did no work */
-#define NF_DEVERR_RANGE 6     /* nf_prefill_attn: a K or V scale whose dequantised codes leave the
-                                 fp16 range the kernel computes in (the results are not finite) */
+#define NF_DEVERR_RANGE 6     /* prefill calls: a K or V scale whose dequantised codes leave the
+                                 fp16 range the kernel computes in, or scores above 4.6e7 (the
+                                 results are not finite) */
 #define NF_DEVERR_CONFLICT 7  /* nf_kv_fork, nf_kv_copy_blocks: a pair whose destination is another
                                  pair's source or destination (the pair was not carried out) */
 #define NF_DEVERR_POOL 8      /* nf_kv_reserve, nf_kv_fork: not enough free blocks */
@@ -347,8 +348,9 @@ nf_status nf_attn_combine_packed(const float *parts, int32_t n_splits, int32_t r
  *   range the kernel holds them in: K scales <= 515.5 (127 x 515.5 < 65504)
  *   and V scales <= 9352 (7 x 9352 < 65504), that is K and V inputs of
  *   magnitude below about 65500.  A larger scale of a key the call reads is
- *   recorded as NF_DEVERR_RANGE (and the affected outputs are not finite);
- *   nf_decode_attn has no such limit.
+ *   recorded as NF_DEVERR_RANGE (and the affected outputs are not finite), and
+ *   so is a query row whose largest score (q . k x softmax_scale) is beyond
+ *   2^26 ln 2 = 4.6e7 in magnitude; nf_decode_attn has no such limits.
  * Numerics: each query row is scaled to max |q| = 1 and rounded to fp16 once
  *   (a row whose max |q| is at most 2^-120 counts as zeros); K and V are
  *   dequantised to fp16 (code x scale, one rounding each); the softmax weights

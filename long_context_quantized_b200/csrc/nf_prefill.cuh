@@ -85,6 +85,10 @@ constexpr int kTcThreads = 512;
 constexpr int kTcRows = 256;   // query rows per CTA (two MMA tiles of 128)
 constexpr int kTcKeys = 64;    // keys per K/V tile (N of S = Q.K^T, K of O += P.V)
 constexpr float kTcLazy = 8.0f;
+// Largest running max (in powers of two) the kernels answer for.  A weight is 2^(s
+// qf - m) with one FMA, and m is the rounded product: at 2^26 the two differ by up
+// to 4, so that weights stay below 2^12; at 2^28 fp16 weights may overflow or vanish.
+constexpr float kTcMaxScore = 0x1p26f;
 constexpr uint32_t kTcIdescQK = umma_idesc_f16(128, 64, false);   // B = K rows, K-major
 constexpr uint32_t kTcIdescPV = umma_idesc_f16(128, 128, true);   // B = V rows, MN-major
 
@@ -494,6 +498,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
                     }
                 }
             }
+            if (m_run != -INFINITY && fabsf(m_run) > kTcMaxScore) report(NF_DEVERR_RANGE);
             if (dst && p.out_lse)
                 p.out_lse[out_row(row)] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
         }

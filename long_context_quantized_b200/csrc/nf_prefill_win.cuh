@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_win_kernel(const __grid
                     }
                 }
             }
+            if (m_run != -INFINITY && fabsf(m_run) > kTcMaxScore) report(NF_DEVERR_RANGE);
             if (row < p.rows && p.out_lse && hf == 0)
                 p.out_lse[out_row(row - r0)] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
         }

@@ -331,6 +331,29 @@ def test_prefill_window_range_of_scales(plane, bits, error):
             assert torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("full", [False, True], ids=["windowed", "full"])
+def test_prefill_scores_beyond_its_range_are_reported(full):
+    """Both prefill kernels answer for rows whose largest score is below 2^26 (in powers of two) and say where one
+    is not; a query that is not a number is not such a row."""
+    for gain, err in ((1e6, 0), (1e9, nf.NF_DEVERR_RANGE), (1e30, nf.NF_DEVERR_RANGE), (float("nan"), 0)):
+        c = Case(nf.NF_KV_K8V4, [900, 500], n_q=40)
+        window, n_sink = (10 ** 6, 0) if full else (300, 4)
+        c.q = (c.q.float() * gain).bfloat16()
+        if full:
+            out = torch.empty(c.q.shape, device="cuda")
+            nf.nf_prefill_attn(c.kv, c.q, c.table, c.lens, c.max_len, SCALE, True, out, c.lse)
+            torch.cuda.synchronize()
+        else:
+            out = c.run(window, n_sink, prefill=True)
+        assert nf.nf_get_device_error() == err
+        if gain == 1e6:
+            _, lse, _ = ref.window_attention(c.kv, c.q, c.np_table, c.seqlens, window, n_sink, SCALE)
+            assert np.abs(lse).max() < 2.0 ** 26 * math.log(2)
+            assert torch.isfinite(out).all() and torch.isfinite(c.lse).all()
+            # a mean of values (weights and values rounded to fp16 once each)
+            assert out.abs().max().item() <= np.abs(ref.open_pool(c.kv)[1]).max() * (1 + 2.0 ** -9)
+
+
 def test_prefill_window_errors():
     c = Case(nf.NF_KV_K8V4, [9, 500], n_q=10)
     c.check(64, 4, prefill=True, errors=nf.NF_DEVERR_SEQLEN)
