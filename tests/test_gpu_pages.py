@@ -357,6 +357,51 @@ def test_captured_turn():
     assert nf.nf_get_device_error() == 0
 
 
+def test_captured_fork_and_compact():
+    """Fork, release of a source and compaction in one graph, replayed on three states."""
+    layers = layers_of(nf.NF_KV_K8V4, 2, 40, 2)
+    r, t, n = dev(np.zeros(40)), dev(np.full((6, 5), -1)), dev(np.zeros(6))
+    src, dst, ws = dev([0, 0, 1]), dev([3, 4, 5]), workspace(40, 3)
+    frm, to = dev([0] * 6), dev([0, 5 * 256, 0, 0, 0, 0])
+
+    def call():
+        nf.nf_kv_fork(layers, r, t, src, dst, n, ws)
+        nf.nf_kv_release(r, t, frm, to)
+        nf.nf_kv_compact(layers, r, t, ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seed in range(3):
+        rng = np.random.default_rng(seed)
+        lens = [int(x) for x in rng.integers(0, 5 * 256 + 1, 2)] + [0] * 4
+        table, ids = np.full((6, 5), -1, np.int32), rng.permutation(40)
+        for row in (0, 1):
+            pages = -(-lens[row] // 256)
+            table[row, :pages] = ids[5 * row:5 * row + pages]
+        refs = np.zeros(40, np.int32)
+        np.add.at(refs, table[table >= 0], 1)
+        r.copy_(dev(refs)), t.copy_(dev(table)), n.copy_(dev(lens))
+        was = bytes_of(layers)
+        graph.replay()
+        want = ref.Pages(refs, table, lens)
+        copies = want.fork([0, 0, 1], [3, 4, 5])
+        want.release([0] * 6, [0, 5 * 256, 0, 0, 0, 0])
+        moves = want.compact()
+        same(r, t, want, n)
+        # the copies first, then the moves: what each moved block held after the copies
+        held = dict((d, s) for s, d in copies)
+        final = {d: held.get(s, s) for s, d in moves}
+        still = {d: s for d, s in held.items() if d not in final}
+        same_bytes(layers, was, [(s, d) for d, s in {**still, **final}.items()])
+        assert nf.nf_get_device_error() == 0
+
+
 def test_pages_binding_refusals():
     layers = layers_of(nf.NF_KV_K8V4, 1, 4, 1)
     refs, table, rows = dev(np.zeros(4)), dev(np.full((2, 3), -1)), dev([0, 0])

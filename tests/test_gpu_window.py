@@ -402,6 +402,39 @@ def test_window_calls_in_a_graph_follow_the_lengths():
     assert nf.nf_get_device_error() == 0
 
 
+def test_prefill_window_in_a_graph_follows_the_lengths():
+    """Captured once, replayed after the lengths changed (an unused row among them)."""
+    c = Case(nf.NF_KV_K8V4, [1300, 900], n_q=150)
+    table, out = c.table, torch.empty(c.q.shape, device="cuda")
+
+    def call():
+        nf.nf_prefill_attn_window(c.kv, c.q, table, c.lens, c.max_len, 400, 70, SCALE, out, c.lse)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        call()
+    for seqlens in ([1300, 900], [150, 0], [777, 512]):
+        c.lens.copy_(torch.tensor(seqlens, dtype=torch.int32))
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        o, _, parts = ref.window_attention(c.kv, c.q, c.np_table, seqlens, 400, 70, SCALE)
+        ref.check_out(out, o, ref.prefill_tolerance(parts))
+    assert nf.nf_get_device_error() == 0
+
+
+@pytest.mark.parametrize("n_q, hq, hkv", [(1, 300, 1), (5, 300, 1), (3, 513, 3), (1, 70, 70), (2, 4096, 2)])
+def test_prefill_window_groups_of_any_size(n_q, hq, hkv):
+    """Rows of a position that span tiles, and positions that share one with a fraction of the next."""
+    Case(nf.NF_KV_K8V4, [700], n_q=n_q, hq=hq, hkv=hkv).check(200, 5, torch.bfloat16, prefill=True)
+
+
 def test_far_pages_of_a_large_pool():
     """Blocks behind the first 4 GiB of a plane: append, decode, prefill and copies."""
     heads, blocks = 8, 17000  # K: 256 KiB a block, 4.15 GiB
