@@ -224,7 +224,8 @@ size_t nf_decode_attn_workspace_size(int32_t batch, int32_t n_q, int32_t num_q_h
  *   tensor-core P.V product; scores, softmax statistics and accumulators are
  *   fp32.  (K8V8: the same, the int8 V codes exact in fp16 likewise.  fp8:
  *   the e4m3 codes are exact in fp16; S = Q . K^T uses fp16 products with each
- *   query row split as q = s (hi + lo), s = max|q|, hi and lo fp16.  bf16
+ *   query row split as q = s (hi + lo), s = max|q|, hi and lo fp16, a row
+ *   with s at most 2^-120 counting as zeros.  bf16
  *   cache: bf16 products, the fp32 query and the weights split into bf16 high
  *   and low parts.)  With 9 to 32 query rows per kv-head, K8/V4, K8V8 and fp8
  *   run on the tcgen05 tensor cores instead: the same two-digit Q . K for
@@ -385,7 +386,9 @@ nf_status nf_prefill_attn(const nf_kv_layer *kv, const void *q, int32_t q_dtype,
  *   Table entries of pages that no query sees a key of are not used, so they
  *     may be -1 (nf_kv_release).  The bytes of keys that no query sees are
  *     read only where they share a 32-key chunk with seen ones, and take no
- *     part in the result, whatever they are.
+ *     part in the result, whatever they are.  (A key that one query of the call
+ *     sees and another does not has weight 0 in the other's row, so its value
+ *     must be finite: 0 times a value that is not finite is not a number.)
  *   softmax_scale > 0; max_seqlen <= 2^30.
  *   Up to 64 rows per kv-head (group * n_q); 9 to 32 of them over K8/V4, K8V8 and
  *     fp8 pools run on tcgen05, as nf_decode_attn's do.

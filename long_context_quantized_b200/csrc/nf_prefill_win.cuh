@@ -13,8 +13,8 @@
 //   on an edge of the window are masked.
 // Roles:
 //   warps 0-15  softmax: eight warps per MMA tile, two threads per row, each with 32
-//              of a key tile's 64 scores.  They stage the query rows (scaled to max
-//              |q| = 1, fp16) once.  Per key tile a thread reads its scores from
+//              of a key tile's 64 scores.  They stage the query rows (scaled by a
+//              power of two to max |q| in [1, 2), fp16) once.  Per key tile a thread reads its scores from
 //              tensor memory into registers at once and frees them for the next S;
 //              the two threads of a row agree on whether its max rises (a barrier
 //              with an OR over the two warps), then write their weights as the fp16
@@ -34,11 +34,12 @@
 // What bounds it: a softmax thread's chain per 64-key tile, about 1.1 us -- the wait
 // for S, its load, the pair's barrier, the exponentials (four warps share a
 // sub-partition's MUFU: 1024 cycles of the 2100) and the store of P -- against
-// 0.55 us of MMA work for the two tiles at the measured 1692 TFLOP/s.  Without the
+// 0.73 us of MMA work for the two tiles (8.4 MFLOP at an SM's share of the measured
+// 1692 TFLOP/s), so the MMAs are not far behind the chain.  Without the
 // exponentials a launch takes 0.90, without the barrier 0.92, without the
 // converters 0.99 of its time.  Measured (32 / 4 heads, one B200, launches back to
 // back): a chunk of 1024 queries at 180224 keys, window 4096, 82 us (0.50 of the
-// 1692 TFLOP/s); a prompt of 8192 with window 2048, 307 us (0.46; a CTA's start
+// 1692 TFLOP/s); a prompt of 8192 with window 2048, 309 us (0.46; a CTA's start
 // and end are 15% of its 45 us).
 // Choices measured on the same two cases:
 //   P in tensor memory, S freed as soon as it is in registers, 16 softmax warps
